@@ -89,7 +89,15 @@ typedef enum {
   PA_ERR_SCRATCH = -7      /* the problem needs more scratch than paged_attn_decode_noalloc holds */
 } pa_status;
 
-typedef enum { PA_KV_BF16 = 0, PA_KV_FP8_E4M3 = 1, PA_KV_NVFP4 = 2 } pa_kv_dtype;
+/* PA_KV_INT8_BLOCK, PA_KV_FP8_BLOCK: 8-bit codes (int8, e4m3) with one fp32 scale per block of
+ * consecutive tokens and kv head, for K and V each; written by paged_attn_append_kv_block. */
+typedef enum {
+  PA_KV_BF16 = 0,
+  PA_KV_FP8_E4M3 = 1,
+  PA_KV_NVFP4 = 2,
+  PA_KV_INT8_BLOCK = 3,
+  PA_KV_FP8_BLOCK = 4
+} pa_kv_dtype;
 
 /* Dequantisation scales of the KV cache (all device pointers).
  *  PA_KV_BF16:      all fields ignored (may be NULL).
@@ -100,11 +108,21 @@ typedef enum { PA_KV_BF16 = 0, PA_KV_FP8_E4M3 = 1, PA_KV_NVFP4 = 2 } pa_kv_dtype
  *                   then [Hkv][page_size][head_dim_vo/16] V scales (e4m3 bytes), i.e.
  *                   the contiguous [all-data | all-SF] arrangement;
  *                   K^ = e2m1(nibble) * e4m3(sf) * k_scale (likewise V).
- *                   16-byte aligned. */
+ *                   16-byte aligned.
+ *  PA_KV_INT8_BLOCK, PA_KV_FP8_BLOCK: block_scales: fp32
+ *                   [num_pages][2][Hkv][page_size / block_tokens] (0: K, 1: V), block i of a
+ *                   page and head being its slots [i * block_tokens, (i + 1) * block_tokens);
+ *                   block_tokens a power of two, at most page_size;
+ *                   K^ = code(K) * block_scales[page][0][head][slot / block_tokens]
+ *                   (likewise V), code an int8 or an e4m3 value.  4-byte aligned.  k_scale,
+ *                   v_scale and sf are ignored.  Scales of blocks without a token are not
+ *                   used (they may hold anything). */
 typedef struct {
   const float* k_scale;
   const float* v_scale;
   const uint8_t* sf;
+  const float* block_scales; /* this field and the next are read for the block dtypes only */
+  int block_tokens;
 } pa_kv_scales;
 
 /*
@@ -116,6 +134,10 @@ typedef struct {
  * each sequence is cut into page-aligned chunks on the device; chunks of one sequence
  * write partial (O, m, l) to the workspace that a merge kernel combines by their lse
  * weights.
+ *
+ * With block scales, a key's K scale multiplies its fp32 score and its V scale its
+ * probability in fp32, relative to a power of two that follows the largest V scale of the
+ * chunk so far, before the probability is rounded to f16; codes enter the MMAs exactly.
  *
  * Supported: (head_dim_qk, head_dim_vo) in {(512,512), (512,256), (256,256)};
  * num_qo_heads / num_kv_heads in [1, 16]; page_size in {1,2,4,8,16,32,64};
@@ -150,7 +172,9 @@ int paged_attn_decode(const void* q, const void* kv_cache, const int32_t* kv_ind
  * are exact).  Page sizes 1, 2 and 4 (any dtype): the pages are read from a bf16 copy
  * that pads each page to 8 rows per kv head (num_pages * num_kv_heads * 8 *
  * (head_dim_qk + head_dim_vo) * 2 bytes), under the same limit; beyond it the call
- * returns PA_ERR_UNSUPPORTED.  When the
+ * returns PA_ERR_UNSUPPORTED.  The block dtypes follow the same rules: their copy holds the
+ * codes' values (K in bf16, V in f16, both exact), and the scales are applied to scores and
+ * probabilities as in paged_attn_decode.  When the
  * (query tile, kv head) items are fewer than the SMs (a few new tokens over a long
  * prefix), the device planner may split long KV ranges into chunks whose fp32 partials a
  * merge kernel combines (paged_attn_set_prefill_split_kv); the workspace then also holds
@@ -231,6 +255,89 @@ int paged_attn_append_kv(const void* k_new, const void* v_new, const int32_t* ap
                          int num_pages, int num_kv_heads, int head_dim_qk, int head_dim_vo,
                          int page_size, int kv_dtype, const float* k_scale,
                          const float* v_scale, uint8_t* sf, void* stream);
+
+/*
+ * paged_attn_append_kv_block -- paged_attn_append_kv for the block dtypes: writes the codes of
+ * the new tokens and finds the scales of the blocks they fall into from the values, so no
+ * calibration is needed.
+ *
+ * k_new, v_new, append_indptr, total_new and the page table are those of
+ * paged_attn_append_kv, except that append_indptr[batch] may be below total_new: rows behind
+ * the last sequence are ignored.  scales is the block_scales pool that the attention calls
+ * read, here updated.  A block that receives new tokens gets, for K and V of each kv head,
+ *   s = max(s_old, amax * RN(1 / C))    C = 127 (PA_KV_INT8_BLOCK) or 448 (PA_KV_FP8_BLOCK);
+ *                                       amax: the largest finite |x| of its new values; s_old:
+ *                                       its scale so far, or 0 if it holds no earlier token of
+ *                                       the sequence (what the pool held is then not read)
+ *   r = min(RN(1 / s), FLT_MAX)
+ *   code(x) = RN(x * r), rounded to the nearest int8 in [-127, 127] or e4m3 value (ties to
+ *             even, saturating); 0 if s = 0; a NaN gives 0 (int8) or a NaN code (e4m3)
+ * and, if s > s_old > 0, the codes of its earlier tokens become code' = RN(code * RN(s_old *
+ * r)) rounded the same way: each such growth adds at most half a step of the grown scale to
+ * their error (int8), and a block grows at most once per append.  Nothing else in the cache
+ * or the pool is written.  Two sequences of one batch must not append into the same page.
+ * kv_dtype PA_KV_INT8_BLOCK or PA_KV_FP8_BLOCK; block_tokens a power of two, at most
+ * page_size.  A row whose position or page id is out of range is skipped with its block and
+ * sets the device error word, as in paged_attn_append_kv.
+ * Returns PA_OK, or PA_ERR_INVALID_ARG / PA_ERR_UNSUPPORTED / PA_ERR_ALIGNMENT / PA_ERR_CUDA;
+ * nothing is launched on error.
+ */
+int paged_attn_append_kv_block(const void* k_new, const void* v_new,
+                               const int32_t* append_indptr, int total_new, void* kv_cache,
+                               const int32_t* kv_indptr, const int32_t* kv_indices,
+                               const int32_t* kv_last_page_len, int batch, int num_pages,
+                               int num_kv_heads, int head_dim_qk, int head_dim_vo, int page_size,
+                               int kv_dtype, float* scales, int block_tokens, void* stream);
+
+/*
+ * paged_attn_resize_tables, paged_attn_build_tables -- page tables on the GPU.  (No
+ * counterpart in the pages: their engines build them on the host.)  A caller that keeps one
+ * block-table row per request and a free list of pages on the device runs a step, captured
+ * into a CUDA graph or not, without reading a length back to the host:
+ *   paged_attn_resize_tables   requests grow or shrink; pages move between free list and rows
+ *   paged_attn_build_tables    the page table and the slots of a batch from rows and lengths
+ *
+ * block_table int32 [rows][table_stride], of each row the first max_pages entries are used:
+ * entry i of a request's row is the page of its tokens [i * page_size, (i + 1) * page_size).
+ * kv_lens int32 [rows]: each request's tokens; ceil(len / page_size) entries of its row are
+ * in use.  row_ids int32 [batch]: the row of each sequence of the batch (distinct; a negative
+ * id is padding: a sequence without tokens), or NULL: sequence b has row b (batch <= rows).
+ * page_size a power of two up to 64; max_pages * page_size below 2^31.
+ *
+ * resize: sequence b's length changes by deltas[b] (int32 [batch], any sign; -len releases
+ * the request).  free_pages int32 [free_size], the first *free_count entries free.  Pages no
+ * longer needed are appended to the free list in batch order, each row's in table order; then
+ * new pages are taken from its end, the last entry first, in the same order; kv_lens and
+ * *free_count are updated.  Entries of rows and of the free list that are not written keep
+ * what they held.  If a row id is >= rows, a length would leave [0, max_pages * page_size],
+ * the free list would overflow or run out, nothing is changed at all and the device error
+ * word is set (paged_attn_check_device_error).
+ *
+ * build: new_counts int32 [batch]: the last max(0, new_counts[b]) tokens of sequence b are
+ * new.  Writes kv_indptr [batch + 1], kv_indices (the used entries only), kv_last_page_len
+ * [batch] (0 for a sequence without tokens) and new_indptr [batch + 1] (the append's
+ * append_indptr, the prefill's qo_indptr); and, unless NULL, for each new token, in
+ * new_indptr's order, slot_map (int64: page * page_size + slot) and positions (int32: its
+ * position in the sequence), both [num_tokens], -1 behind the last new token.  A sequence
+ * whose row id is >= rows, whose length is outside [0, max_pages * page_size] or that has
+ * more new tokens than tokens is listed without tokens; a page id outside [0, num_pages) is
+ * listed as page 0 and slot -1; if the pages exceed max_indices or the new tokens num_tokens,
+ * every sequence is listed without tokens.  Each of these sets the device error word.
+ *
+ * Both return PA_OK, or PA_ERR_INVALID_ARG (a null required pointer, a negative size,
+ * table_stride < max_pages), PA_ERR_UNSUPPORTED (another page size, max_pages * page_size of
+ * 2^31 or more), PA_ERR_ALIGNMENT (int32 arrays 4 bytes, slot_map 8) or PA_ERR_CUDA.
+ */
+int paged_attn_resize_tables(int32_t* block_table, int rows, int max_pages, int table_stride,
+                             const int32_t* row_ids, int32_t* kv_lens, const int32_t* deltas,
+                             int batch, int page_size, int32_t* free_pages, int free_size,
+                             int32_t* free_count, void* stream);
+int paged_attn_build_tables(const int32_t* block_table, int rows, int max_pages, int table_stride,
+                            const int32_t* row_ids, const int32_t* kv_lens,
+                            const int32_t* new_counts, int batch, int page_size, int num_pages,
+                            int32_t* kv_indptr, int32_t* kv_indices, int max_indices,
+                            int32_t* kv_last_page_len, int32_t* new_indptr, int64_t* slot_map,
+                            int32_t* positions, int num_tokens, void* stream);
 
 /* Human-readable text of a pa_status value (static storage, never NULL). */
 const char* paged_attn_status_string(int status);

@@ -21,7 +21,7 @@ import torch
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", "libpaged_attn.so")
 
-PA_KV_BF16, PA_KV_FP8_E4M3, PA_KV_NVFP4 = 0, 1, 2
+PA_KV_BF16, PA_KV_FP8_E4M3, PA_KV_NVFP4, PA_KV_INT8_BLOCK, PA_KV_FP8_BLOCK = 0, 1, 2, 3, 4
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_ALIGNMENT = 0, -1, -2, -3
 PA_ERR_SMEM, PA_ERR_CUDA, PA_ERR_DEVICE, PA_ERR_SCRATCH = -4, -5, -6, -7
 PA_NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -33,7 +33,8 @@ EXPORTED = ("paged_attn_decode", "paged_attn_prefill", "paged_attn_status_string
             "paged_attn_profile_begin", "paged_attn_profile_end", "paged_attn_decode_noalloc",
             "paged_attn_set_prefill_dequant_limit", "paged_attn_set_prefill_cta_pairs",
             "paged_attn_append_kv", "paged_attn_prefill_custom_mask", "paged_attn_set_prefill_split_kv",
-            "paged_attn_debug_set_error_word")
+            "paged_attn_debug_set_error_word", "paged_attn_append_kv_block", "paged_attn_resize_tables",
+            "paged_attn_build_tables")
 
 _lib = None
 
@@ -45,7 +46,8 @@ class PagedAttnError(RuntimeError):
 
 
 class _Scales(ctypes.Structure):
-    _fields_ = [("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("sf", ctypes.c_void_p)]
+    _fields_ = [("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("sf", ctypes.c_void_p),
+                ("block_scales", ctypes.c_void_p), ("block_tokens", ctypes.c_int)]
 
 
 def load(path: Optional[str] = None):
@@ -69,6 +71,14 @@ def load(path: Optional[str] = None):
     lib.paged_attn_append_kv.restype = i32
     lib.paged_attn_append_kv.argtypes = [vp, vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32,
                                          vp, vp, vp, vp]
+    lib.paged_attn_append_kv_block.restype = i32
+    lib.paged_attn_append_kv_block.argtypes = [vp, vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32,
+                                               vp, i32, vp]
+    lib.paged_attn_resize_tables.restype = i32
+    lib.paged_attn_resize_tables.argtypes = [vp, i32, i32, i32, vp, vp, vp, i32, i32, vp, i32, vp, vp]
+    lib.paged_attn_build_tables.restype = i32
+    lib.paged_attn_build_tables.argtypes = [vp, i32, i32, i32, vp, vp, vp, i32, i32, i32, vp, vp, i32, vp, vp, vp, vp,
+                                            i32, vp]
     lib.paged_attn_prefill_custom_mask.restype = i32
     lib.paged_attn_prefill_custom_mask.argtypes = list(lib.paged_attn_prefill.argtypes[:-1]) + [vp, vp, vp]
     lib.paged_attn_status_string.restype = ctypes.c_char_p
@@ -121,12 +131,30 @@ def _stream(stream):
 
 
 def _x2(kv_dtype: int) -> int:
-    return {PA_KV_BF16: 4, PA_KV_FP8_E4M3: 2, PA_KV_NVFP4: 1}[kv_dtype]
+    return {PA_KV_BF16: 4, PA_KV_FP8_E4M3: 2, PA_KV_NVFP4: 1, PA_KV_INT8_BLOCK: 2, PA_KV_FP8_BLOCK: 2}[kv_dtype]
 
 
-def _scales(kv_dtype, k_scale, v_scale, sf):
+def _typed(t: torch.Tensor, dtype: torch.dtype, numel: int, what: str):
+    """_ptr(t) of a tensor that must have this dtype and at least numel elements."""
+    if t.dtype != dtype or t.numel() < numel:
+        raise ValueError(f"{what}: expected at least {numel} elements of {dtype}, got {t.numel()} of {t.dtype}")
+    return _ptr(t)
+
+
+def _block_scales(block_scales, block_tokens, num_pages, num_kv_heads, page_size):
+    """The pointer of a block_scales pool, after checking that it covers the pages."""
+    if block_scales is None or not 1 <= block_tokens <= page_size:
+        raise ValueError("the block dtypes need block_scales and 1 <= block_tokens <= page_size")
+    return _typed(block_scales, torch.float32, num_pages * 2 * num_kv_heads * (page_size // block_tokens),
+                  "block_scales")
+
+
+def _scales(kv_dtype, k_scale, v_scale, sf, block_scales, block_tokens, num_pages, num_kv_heads, page_size):
     sc = _Scales(None, None, None)
-    if kv_dtype != PA_KV_BF16:
+    if kv_dtype in (PA_KV_INT8_BLOCK, PA_KV_FP8_BLOCK):
+        sc.block_scales = _block_scales(block_scales, block_tokens, num_pages, num_kv_heads, page_size)
+        sc.block_tokens = block_tokens
+    elif kv_dtype != PA_KV_BF16:
         sc.k_scale = _ptr(k_scale)
         sc.v_scale = _ptr(v_scale)
         sc.sf = _ptr(sf)
@@ -145,8 +173,10 @@ def paged_attn_decode(q: torch.Tensor, kv_cache: torch.Tensor, kv_indptr: torch.
                       k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
                       sf: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
                       lse: Optional[torch.Tensor] = None, num_pages: Optional[int] = None,
-                      stream=None, return_lse: bool = True) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
-    """Decode: q [batch, Hq, head_dim_qk] bf16 -> out [batch, Hq, head_dim_vo] bf16, lse [batch, Hq]."""
+                      stream=None, return_lse: bool = True, block_scales: Optional[torch.Tensor] = None,
+                      block_tokens: int = 0) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Decode: q [batch, Hq, head_dim_qk] bf16 -> out [batch, Hq, head_dim_vo] bf16, lse [batch, Hq].
+    block_scales [num_pages, 2, Hkv, page_size / block_tokens] (fp32) for the block dtypes."""
     batch, hq, dqk = q.shape
     if num_pages is None:
         num_pages = _num_pages(kv_cache, num_kv_heads, dqk, head_dim_vo, page_size, kv_dtype)
@@ -154,7 +184,7 @@ def paged_attn_decode(q: torch.Tensor, kv_cache: torch.Tensor, kv_indptr: torch.
         out = torch.empty(batch, hq, head_dim_vo, dtype=torch.bfloat16, device=q.device)
     if lse is None and return_lse:
         lse = torch.empty(batch, hq, dtype=torch.float32, device=q.device)
-    sc = _scales(kv_dtype, k_scale, v_scale, sf)
+    sc = _scales(kv_dtype, k_scale, v_scale, sf, block_scales, block_tokens, num_pages, num_kv_heads, page_size)
     st = load().paged_attn_decode(_ptr(q), _ptr(kv_cache), _ptr(kv_indptr), _ptr(kv_indices),
                                   _ptr(kv_last_page_len), batch, num_pages, hq, num_kv_heads, dqk,
                                   head_dim_vo, page_size, float(sm_scale), window_left, kv_dtype,
@@ -170,14 +200,15 @@ def paged_attn_decode_noalloc(q: torch.Tensor, kv_cache: torch.Tensor, kv_indptr
                               sm_scale: float, window_left: int = -1, kv_dtype: int = PA_KV_BF16,
                               k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
                               sf: Optional[torch.Tensor] = None, num_pages: Optional[int] = None,
-                              stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+                              stream=None, block_scales: Optional[torch.Tensor] = None,
+                              block_tokens: int = 0) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Decode for callers that cannot allocate device memory: the library uses only its
     fixed scratch array, and the caller passes ``out`` (and ``lse``) already allocated.
     Overlapping calls race on that array; serialise them."""
     batch, hq, dqk = q.shape
     if num_pages is None:
         num_pages = _num_pages(kv_cache, num_kv_heads, dqk, head_dim_vo, page_size, kv_dtype)
-    sc = _scales(kv_dtype, k_scale, v_scale, sf)
+    sc = _scales(kv_dtype, k_scale, v_scale, sf, block_scales, block_tokens, num_pages, num_kv_heads, page_size)
     st = load().paged_attn_decode_noalloc(_ptr(q), _ptr(kv_cache), _ptr(kv_indptr), _ptr(kv_indices),
                                           _ptr(kv_last_page_len), batch, num_pages, hq, num_kv_heads, dqk,
                                           head_dim_vo, page_size, float(sm_scale), window_left, kv_dtype,
@@ -196,10 +227,11 @@ def paged_attn_prefill(q: torch.Tensor, qo_indptr: torch.Tensor, kv_cache: torch
                        out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                        num_pages: Optional[int] = None, stream=None,
                        return_lse: bool = True, custom_mask: Optional[torch.Tensor] = None,
-                       mask_indptr: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+                       mask_indptr: Optional[torch.Tensor] = None, block_scales: Optional[torch.Tensor] = None,
+                       block_tokens: int = 0) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Prefill: q [total_q, Hq, head_dim_qk] bf16 -> out [total_q, Hq, head_dim_vo] bf16.
     custom_mask (uint8 bits) with mask_indptr (int64 byte offsets per sequence) selects
-    paged_attn_prefill_custom_mask."""
+    paged_attn_prefill_custom_mask.  block_scales as for paged_attn_decode."""
     total_q, hq, dqk = q.shape
     batch = qo_indptr.numel() - 1
     if num_pages is None:
@@ -208,7 +240,7 @@ def paged_attn_prefill(q: torch.Tensor, qo_indptr: torch.Tensor, kv_cache: torch
         out = torch.empty(total_q, hq, head_dim_vo, dtype=torch.bfloat16, device=q.device)
     if lse is None and return_lse:
         lse = torch.empty(total_q, hq, dtype=torch.float32, device=q.device)
-    sc = _scales(kv_dtype, k_scale, v_scale, sf)
+    sc = _scales(kv_dtype, k_scale, v_scale, sf, block_scales, block_tokens, num_pages, num_kv_heads, page_size)
     args = (_ptr(q), _ptr(qo_indptr), total_q, _ptr(kv_cache), _ptr(kv_indptr), _ptr(kv_indices),
             _ptr(kv_last_page_len), batch, num_pages, hq, num_kv_heads, dqk, head_dim_vo, page_size,
             float(sm_scale), window_left, int(bool(causal)), kv_dtype, ctypes.byref(sc), _ptr(out), _ptr(lse))
@@ -242,6 +274,85 @@ def paged_attn_append_kv(k_new: torch.Tensor, v_new: torch.Tensor, append_indptr
                                      _ptr(v_scale), _ptr(sf), _stream(stream))
     if st != PA_OK:
         raise PagedAttnError(st, "paged_attn_append_kv")
+
+
+def paged_attn_append_kv_block(k_new: torch.Tensor, v_new: torch.Tensor, append_indptr: torch.Tensor,
+                               kv_cache: torch.Tensor, kv_indptr: torch.Tensor, kv_indices: torch.Tensor,
+                               kv_last_page_len: torch.Tensor, block_scales: torch.Tensor, *, page_size: int,
+                               block_tokens: int, kv_dtype: int = PA_KV_INT8_BLOCK, num_pages: Optional[int] = None,
+                               stream=None) -> None:
+    """Write k_new [total_new, Hkv, head_dim_qk] / v_new [total_new, Hkv, head_dim_vo] (bf16) as
+    8-bit codes of the last tokens of each sequence, and the scales of the blocks they fall
+    into: block_scales [num_pages, 2, Hkv, page_size / block_tokens] (fp32)."""
+    total_new, hkv, dqk = k_new.shape
+    dvo = v_new.shape[2]
+    if tuple(v_new.shape[:2]) != (total_new, hkv) or k_new.dtype != torch.bfloat16 or v_new.dtype != torch.bfloat16:
+        raise ValueError("k_new and v_new must be bf16 with the same rows and kv heads")
+    batch = append_indptr.numel() - 1
+    if num_pages is None:
+        num_pages = _num_pages(kv_cache, hkv, dqk, dvo, page_size, kv_dtype)
+    st = load().paged_attn_append_kv_block(
+        _ptr(k_new), _ptr(v_new), _ptr(append_indptr), total_new, _ptr(kv_cache), _ptr(kv_indptr), _ptr(kv_indices), _ptr(kv_last_page_len),
+        batch, num_pages, hkv, dqk, dvo, page_size, kv_dtype,
+        _block_scales(block_scales, block_tokens, num_pages, hkv, page_size), block_tokens, _stream(stream))
+    if st != PA_OK:
+        raise PagedAttnError(st, "paged_attn_append_kv_block")
+
+
+def _table(block_table: torch.Tensor):
+    """(pointer, rows, max_pages, row stride) of an int32 block table whose rows are contiguous."""
+    if not block_table.is_cuda:
+        raise ValueError("tensor arguments must be CUDA tensors")
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or \
+            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be int32 [rows, max_pages] with contiguous rows")
+    rows, width = block_table.shape
+    return block_table.data_ptr(), rows, width, max(block_table.stride(0), width)
+
+
+def paged_attn_resize_tables(block_table: torch.Tensor, row_ids: Optional[torch.Tensor], kv_lens: torch.Tensor,
+                             deltas: torch.Tensor, free_pages: torch.Tensor, free_count: torch.Tensor, *,
+                             page_size: int, stream=None) -> None:
+    """Change the length of sequence b (row row_ids[b] of block_table [rows, max_pages], or row b)
+    by deltas[b] tokens, moving pages between its row and the free list (free_pages, the first
+    free_count[0] entries free); kv_lens [rows] and free_count [1] are updated.  All int32."""
+    ptr, rows, width, stride = _table(block_table)
+    batch, i32 = deltas.numel(), torch.int32
+    st = load().paged_attn_resize_tables(
+        ptr, rows, width, stride, None if row_ids is None else _typed(row_ids, i32, batch, "row_ids"),
+        _typed(kv_lens, i32, rows, "kv_lens"), _typed(deltas, i32, batch, "deltas"), batch, page_size,
+        _typed(free_pages, i32, 0, "free_pages"), free_pages.numel(), _typed(free_count, i32, 1, "free_count"),
+        _stream(stream))
+    if st != PA_OK:
+        raise PagedAttnError(st, "paged_attn_resize_tables")
+
+
+def paged_attn_build_tables(block_table: torch.Tensor, row_ids: Optional[torch.Tensor], kv_lens: torch.Tensor,
+                            new_counts: torch.Tensor, *, page_size: int, num_pages: int, max_indices: int,
+                            num_tokens: int, out: Optional[Tuple[torch.Tensor, ...]] = None,
+                            stream=None) -> Tuple[torch.Tensor, ...]:
+    """Page table of a batch, its last new_counts[b] tokens per sequence being new:
+    (kv_indptr [batch + 1], kv_indices [max_indices], kv_last_page_len [batch], new_indptr
+    [batch + 1], slot_map int64 [num_tokens], positions [num_tokens]), int32 but for slot_map.
+    max_indices and num_tokens are capacities; ``out`` gives the six tensors to write."""
+    ptr, rows, width, stride = _table(block_table)
+    batch, i32 = new_counts.numel(), torch.int32
+    if out is None:
+        dev = block_table.device
+        sizes = (batch + 1, max_indices, batch, batch + 1)
+        out = tuple(torch.empty(n, dtype=i32, device=dev) for n in sizes) + (
+            torch.empty(num_tokens, dtype=torch.int64, device=dev), torch.empty(num_tokens, dtype=i32, device=dev))
+    indptr, indices, last, new_indptr, slots, positions = out
+    st = load().paged_attn_build_tables(
+        ptr, rows, width, stride, None if row_ids is None else _typed(row_ids, i32, batch, "row_ids"),
+        _typed(kv_lens, i32, rows, "kv_lens"), _typed(new_counts, i32, batch, "new_counts"), batch, page_size,
+        num_pages, _typed(indptr, i32, batch + 1, "kv_indptr"), _typed(indices, i32, max_indices, "kv_indices"),
+        max_indices, _typed(last, i32, batch, "kv_last_page_len"), _typed(new_indptr, i32, batch + 1, "new_indptr"),
+        _typed(slots, torch.int64, num_tokens, "slot_map"), _typed(positions, i32, num_tokens, "positions"),
+        num_tokens, _stream(stream))
+    if st != PA_OK:
+        raise PagedAttnError(st, "paged_attn_build_tables")
+    return out
 
 
 def paged_attn_release_workspace() -> None:

@@ -25,6 +25,7 @@ namespace pa {
 namespace {
 
 thread_local char g_variant[64] = "none";
+const char* const kv_names[5] = {"bf16", "fp8", "nvfp4", "int8_block", "fp8_block"};
 
 // measurement hook state: event pairs recorded around the main kernel of each call
 struct Profile {
@@ -191,7 +192,27 @@ bool make_map_rows(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-int x2_of(int kvt) { return kvt == KV_BF16 ? 4 : (kvt == KV_FP8 ? 2 : 1); }
+int x2_of(int kvt) { return kvt == KV_BF16 ? 4 : (kvt == KV_NVFP4 ? 1 : 2); }
+
+int log2_of(int v) { return 31 - __builtin_clz((unsigned)v); }
+
+// The block scales of a kv_dtype that has them (zeros otherwise).
+BlockScales block_scales(int kv_dtype, const pa_kv_scales* sc, int page_size) {
+  BlockScales b = {};
+  if (kv_block_scaled(kv_dtype)) {
+    b.s = sc->block_scales;
+    b.log2_tokens = log2_of(sc->block_tokens);
+    b.per_head = page_size / sc->block_tokens;
+  }
+  return b;
+}
+
+// The block-scale arguments of a page_size that has been checked.
+int check_block_scales(const float* scales, int block_tokens, int page_size) {
+  if (!scales) return PA_ERR_INVALID_ARG;
+  if (block_tokens < 1 || block_tokens > page_size || (block_tokens & (block_tokens - 1))) return PA_ERR_INVALID_ARG;
+  return (reinterpret_cast<uintptr_t>(scales) & 3) ? PA_ERR_ALIGNMENT : PA_OK;
+}
 
 // Decode chunks of at least about 4 MiB of K and V per kv head (NVFP4: with its scales).
 int decode_min_chunk_pages(int kvt, int dqk, int dvo, int page_size) {
@@ -208,7 +229,7 @@ bool decode_direct(int kvt, int dqk, int dvo, int page_size, long long num_pages
   if (g_decode_direct == 0 || g_forced_chunk_pages > 0) return false;
   if ((long long)batch * hkv > sms) return false;
   if (g_decode_direct == 1) return true;
-  const double per_elem = kvt == PA_KV_BF16 ? 2.0 : (kvt == PA_KV_FP8_E4M3 ? 1.0 : 0.5 + 1.0 / 16.0);
+  const double per_elem = kvt == PA_KV_BF16 ? 2.0 : (kvt == PA_KV_NVFP4 ? 0.5 + 1.0 / 16.0 : 1.0);
   return (double)num_pages * page_size * (dqk + dvo) * per_elem <= 256.0 * 1024.0;
 }
 
@@ -225,8 +246,12 @@ int check_common(const void* q, const void* kv_cache, const int32_t* kv_indptr, 
     return PA_ERR_UNSUPPORTED;
   if (page_size < 1 || page_size > 64 || (page_size & (page_size - 1))) return PA_ERR_UNSUPPORTED;
   if (!std::isfinite(sm_scale) || window_left < -1) return PA_ERR_INVALID_ARG;
-  if (kv_dtype != PA_KV_BF16 && kv_dtype != PA_KV_FP8_E4M3 && kv_dtype != PA_KV_NVFP4) return PA_ERR_INVALID_ARG;
-  if (kv_dtype != PA_KV_BF16) {
+  if (kv_dtype < PA_KV_BF16 || kv_dtype > PA_KV_FP8_BLOCK) return PA_ERR_INVALID_ARG;
+  if (kv_block_scaled(kv_dtype)) {
+    if (!sc) return PA_ERR_INVALID_ARG;
+    const int st = check_block_scales(sc->block_scales, sc->block_tokens, page_size);
+    if (st != PA_OK) return st;
+  } else if (kv_dtype != PA_KV_BF16) {
     if (!sc || !sc->k_scale || !sc->v_scale) return PA_ERR_INVALID_ARG;
     if (!aligned(sc->k_scale, 4) || !aligned(sc->v_scale, 4)) return PA_ERR_ALIGNMENT;
   }
@@ -239,6 +264,20 @@ int check_common(const void* q, const void* kv_cache, const int32_t* kv_indptr, 
   if (lse && !aligned(lse, 4)) return PA_ERR_ALIGNMENT;
   const uint64_t page_bytes = (uint64_t)Hkv * page_size * (dqk + dvo) * x2_of(kv_dtype) / 2;
   if ((uint64_t)num_pages * page_bytes >= (1ull << 46)) return PA_ERR_INVALID_ARG;
+  return PA_OK;
+}
+
+// The arguments that both table calls share (`counts`: per-sequence deltas or new tokens).
+int check_tables(const int32_t* block_table, int rows, int max_pages, int table_stride, const int32_t* row_ids,
+                 const int32_t* kv_lens, const int32_t* counts, int batch, int page_size) {
+  if (batch < 0 || rows < 0 || max_pages < 0 || table_stride < max_pages) return PA_ERR_INVALID_ARG;
+  if (page_size < 1 || page_size > 64 || (page_size & (page_size - 1))) return PA_ERR_UNSUPPORTED;
+  if ((uint64_t)max_pages * page_size >= (1ull << 31)) return PA_ERR_UNSUPPORTED;  // lengths are int32
+  if (batch == 0) return PA_OK;
+  if (!block_table || !kv_lens || !counts) return PA_ERR_INVALID_ARG;
+  if (!row_ids && batch > rows) return PA_ERR_INVALID_ARG;
+  if (!aligned(block_table, 4) || !aligned(row_ids, 4) || !aligned(kv_lens, 4) || !aligned(counts, 4))
+    return PA_ERR_ALIGNMENT;
   return PA_OK;
 }
 
@@ -538,8 +577,10 @@ int paged_attn_decode(const void* q, const void* kv_cache, const int32_t* kv_ind
   p.kv_indptr = kv_indptr;
   p.kv_indices = kv_indices;
   p.kv_last_page_len = kv_last_page_len;
-  p.k_scale = kv_dtype != PA_KV_BF16 ? kv_scales->k_scale : nullptr;
-  p.v_scale = kv_dtype != PA_KV_BF16 ? kv_scales->v_scale : nullptr;
+  const bool per_tensor = kv_dtype == PA_KV_FP8_E4M3 || kv_dtype == PA_KV_NVFP4;
+  p.k_scale = per_tensor ? kv_scales->k_scale : nullptr;
+  p.v_scale = per_tensor ? kv_scales->v_scale : nullptr;
+  p.bs = block_scales(kv_dtype, kv_scales, page_size);
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
   p.err = reinterpret_cast<int*>(ws + kErrOffset);
@@ -573,11 +614,12 @@ int paged_attn_decode(const void* q, const void* kv_cache, const int32_t* kv_ind
   prof_mark(L.stream, true);
   if (kv_dtype == PA_KV_BF16) e = launch_decode_bf16(head_dim_qk, head_dim_vo, hp, L, &name);
   else if (kv_dtype == PA_KV_FP8_E4M3) e = launch_decode_fp8(head_dim_qk, head_dim_vo, hp, L, &name);
+  else if (kv_dtype == PA_KV_INT8_BLOCK) e = launch_decode_int8b(head_dim_qk, head_dim_vo, hp, L, &name);
+  else if (kv_dtype == PA_KV_FP8_BLOCK) e = launch_decode_fp8b(head_dim_qk, head_dim_vo, hp, L, &name);
   else e = launch_decode_nvfp4(head_dim_qk, head_dim_vo, hp, L, &name);
   prof_mark(L.stream, false);
   if (e != cudaSuccess) return PA_ERR_CUDA;
   if (!direct && launch_decode_merge(head_dim_vo, p, L.grid, L.stream) != cudaSuccess) return PA_ERR_CUDA;
-  static const char* kv_names[3] = {"bf16", "fp8", "nvfp4"};
   std::snprintf(g_variant, sizeof g_variant, "%s_%s%s", name, kv_names[kv_dtype], direct ? "_direct" : "");
   return PA_OK;
 }
@@ -608,17 +650,21 @@ int prefill_call(const void* q, const int32_t* qo_indptr, int total_q, const voi
   int smem_optin = 0;
   const int sms = device_sms(&smem_optin);
   if (sms <= 0) return PA_ERR_CUDA;
-  // FP8 / NVFP4: convert the referenced pages once into a bf16 copy and run the bf16
-  // kernel on it, when the copy fits the limit; else convert inside the kernel
+  // FP8 / NVFP4 / 8-bit codes with block scales: convert the referenced pages once into a
+  // 16-bit copy and run the bf16 kernel on it, when the copy fits the limit; else convert
+  // inside the kernel
   const bool quant = kv_dtype != PA_KV_BF16;
   const uint64_t bf16_page = (uint64_t)num_kv_heads * rows_copy * (head_dim_qk + head_dim_vo) * 2;
   const bool dequant = (quant || pad) && (uint64_t)num_pages * bf16_page <= g_prefill_dequant_limit.load();
   if (pad && !dequant) return PA_ERR_UNSUPPORTED;  // the padded copy would exceed the limit
   const int run_kvt = dequant ? (int)PA_KV_BF16 : kv_dtype;
-  if (prefill_smem_bytes(run_kvt, head_dim_qk, head_dim_vo) > smem_optin) return PA_ERR_SMEM;
+  const bool scaled = kv_block_scaled(kv_dtype);
+  const int smem = scaled ? prefill_block_smem_bytes(run_kvt, head_dim_qk, head_dim_vo)
+                          : prefill_smem_bytes(run_kvt, head_dim_qk, head_dim_vo);
+  if (smem > smem_optin) return PA_ERR_SMEM;
   // bf16 kernel (or the bf16 copy): CTA pairs share each MMA and each K/V tile
   int pair_grid = 0;
-  if (run_kvt == PA_KV_BF16 && !pad && g_prefill_pairs.load() == 1)
+  if (run_kvt == PA_KV_BF16 && !pad && !scaled && g_prefill_pairs.load() == 1)
     pair_grid = 2 * std::min(sms / 2, pair_clusters(head_dim_qk, head_dim_vo));
 
   // split KV (short queries over long KV): when even one item per (query tile, kv head)
@@ -652,9 +698,9 @@ int prefill_call(const void* q, const int32_t* qo_indptr, int total_q, const voi
   // the converter warps.
   const void* kv_read = dequant ? static_cast<const void*>(ws + o_shadow) : kv_cache;
   const bool packed = run_kvt != PA_KV_BF16;
-  if (!make_kv_maps(&L.tk, &L.tv, &L.tsfk, &L.tsfv, kv_read, packed ? kv_scales->sf : nullptr, num_pages,
+  if (!make_kv_maps(&L.tk, &L.tv, &L.tsfk, &L.tsfv, kv_read, run_kvt == KV_NVFP4 ? kv_scales->sf : nullptr, num_pages,
                     num_kv_heads, head_dim_qk, head_dim_vo, rows_copy, run_kvt, rows_copy, !packed,
-                    packed ? (run_kvt == KV_FP8 ? 64u : 32u) : 128u))
+                    packed ? (run_kvt == KV_NVFP4 ? 32u : 64u) : 128u))
     return PA_ERR_CUDA;
   // Q as [total_q][Hq][d_qk] bf16 bytes: boxes of [rows_per_tile][group][128 B]
   {
@@ -689,10 +735,12 @@ int prefill_call(const void* q, const int32_t* qo_indptr, int total_q, const voi
   p.kv_indptr = kv_indptr;
   p.kv_indices = kv_indices;
   p.kv_last_page_len = kv_last_page_len;
-  p.k_scale = kv_dtype != PA_KV_BF16 ? kv_scales->k_scale : nullptr;
-  p.v_scale = kv_dtype != PA_KV_BF16 ? kv_scales->v_scale : nullptr;
+  const bool per_tensor = kv_dtype == PA_KV_FP8_E4M3 || kv_dtype == PA_KV_NVFP4;
+  p.k_scale = per_tensor ? kv_scales->k_scale : nullptr;
+  p.v_scale = per_tensor ? kv_scales->v_scale : nullptr;
+  p.bs = block_scales(kv_dtype, kv_scales, page_size);
   p.kv_cache = static_cast<const uint8_t*>(kv_cache);
-  p.sf = kv_scales ? kv_scales->sf : nullptr;
+  p.sf = kv_dtype == PA_KV_NVFP4 ? kv_scales->sf : nullptr;
   p.out = static_cast<uint16_t*>(out);
   p.out_v8 = aligned(out, 32) ? 1 : 0;
   p.lse = lse;
@@ -747,11 +795,11 @@ int prefill_call(const void* q, const int32_t* qo_indptr, int total_q, const voi
     return PA_ERR_CUDA;
   const char* name = "?";
   prof_mark(L.stream, true);
-  cudaError_t e = launch_prefill(run_kvt, head_dim_qk, head_dim_vo, L, &name);
+  cudaError_t e = scaled ? launch_prefill_block(run_kvt, head_dim_qk, head_dim_vo, L, &name)
+                         : launch_prefill(run_kvt, head_dim_qk, head_dim_vo, L, &name);
   prof_mark(L.stream, false);
   if (e != cudaSuccess) return PA_ERR_CUDA;
   if (split && launch_prefill_merge(head_dim_vo, p, sms, L.stream) != cudaSuccess) return PA_ERR_CUDA;
-  static const char* kv_names[3] = {"bf16", "fp8", "nvfp4"};
   std::snprintf(g_variant, sizeof g_variant, "%s_%s%s%s%s", name, kv_names[kv_dtype],
                 pad ? "_padded" : (dequant ? "_dequant" : ""), mask ? "_mask" : "", split ? "_splitkv" : "");
   return PA_OK;
@@ -841,8 +889,140 @@ int paged_attn_append_kv(const void* k_new, const void* v_new, const int32_t* ap
   const cudaError_t e = launch_append_kv(kv_dtype, p, sms, static_cast<cudaStream_t>(stream));
   prof_mark(static_cast<cudaStream_t>(stream), false);
   if (e != cudaSuccess) return PA_ERR_CUDA;
-  static const char* kv_names[3] = {"bf16", "fp8", "nvfp4"};
   std::snprintf(g_variant, sizeof g_variant, "append_kv_%s", kv_names[kv_dtype]);
+  return PA_OK;
+}
+
+int paged_attn_append_kv_block(const void* k_new, const void* v_new, const int32_t* append_indptr, int total_new,
+                               void* kv_cache, const int32_t* kv_indptr, const int32_t* kv_indices,
+                               const int32_t* kv_last_page_len, int batch, int num_pages, int num_kv_heads,
+                               int head_dim_qk, int head_dim_vo, int page_size, int kv_dtype, float* scales,
+                               int block_tokens, void* stream) {
+  if (batch < 0 || total_new < 0 || num_pages < 1 || num_kv_heads < 1) return PA_ERR_INVALID_ARG;
+  if (!kv_block_scaled(kv_dtype)) return PA_ERR_INVALID_ARG;
+  if (!((head_dim_qk == 512 && head_dim_vo == 512) || (head_dim_qk == 512 && head_dim_vo == 256) ||
+        (head_dim_qk == 256 && head_dim_vo == 256)))
+    return PA_ERR_UNSUPPORTED;
+  if (page_size < 1 || page_size > 64 || (page_size & (page_size - 1))) return PA_ERR_UNSUPPORTED;
+  if (batch == 0 || total_new == 0) return PA_OK;
+  if (!k_new || !v_new || !append_indptr || !kv_cache || !kv_indptr || !kv_indices || !kv_last_page_len)
+    return PA_ERR_INVALID_ARG;
+  int st = check_block_scales(scales, block_tokens, page_size);
+  if (st != PA_OK) return st;
+  if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(kv_cache, 16)) return PA_ERR_ALIGNMENT;
+  if (!aligned(append_indptr, 4) || !aligned(kv_indptr, 4) || !aligned(kv_indices, 4) ||
+      !aligned(kv_last_page_len, 4))
+    return PA_ERR_ALIGNMENT;
+  const uint64_t page_bytes = (uint64_t)num_kv_heads * page_size * (head_dim_qk + head_dim_vo);
+  if ((uint64_t)num_pages * page_bytes >= (1ull << 46)) return PA_ERR_INVALID_ARG;
+  char* ws = static_cast<char*>(workspace(kFixedBytes, static_cast<cudaStream_t>(stream), &st));
+  if (!ws) return st;
+  AppendBlockParams p;
+  std::memset(&p, 0, sizeof p);
+  p.k_new = static_cast<const uint16_t*>(k_new);
+  p.v_new = static_cast<const uint16_t*>(v_new);
+  p.append_indptr = append_indptr;
+  p.kv_indptr = kv_indptr;
+  p.kv_indices = kv_indices;
+  p.kv_last_page_len = kv_last_page_len;
+  p.cache = static_cast<uint8_t*>(kv_cache);
+  p.scales = scales;
+  p.err = reinterpret_cast<int*>(ws + kErrOffset);
+  p.log2_tokens = log2_of(block_tokens);
+  p.per_head = page_size / block_tokens;
+  p.batch = batch;
+  p.total_new = total_new;
+  p.num_pages = num_pages;
+  p.Hkv = num_kv_heads;
+  p.d_qk = head_dim_qk;
+  p.d_vo = head_dim_vo;
+  p.page_size = page_size;
+  prof_mark(static_cast<cudaStream_t>(stream), true);
+  const cudaError_t e = launch_append_block(kv_dtype, p, static_cast<cudaStream_t>(stream));
+  prof_mark(static_cast<cudaStream_t>(stream), false);
+  if (e != cudaSuccess) return PA_ERR_CUDA;
+  std::snprintf(g_variant, sizeof g_variant, "append_kv_%s", kv_names[kv_dtype]);
+  return PA_OK;
+}
+
+int paged_attn_resize_tables(int32_t* block_table, int rows, int max_pages, int table_stride, const int32_t* row_ids,
+                             int32_t* kv_lens, const int32_t* deltas, int batch, int page_size, int32_t* free_pages,
+                             int free_size, int32_t* free_count, void* stream) {
+  int st = check_tables(block_table, rows, max_pages, table_stride, row_ids, kv_lens, deltas, batch, page_size);
+  if (st != PA_OK) return st;
+  if (free_size < 0) return PA_ERR_INVALID_ARG;
+  if (batch == 0) return PA_OK;
+  if (!free_pages || !free_count) return PA_ERR_INVALID_ARG;
+  if (!aligned(free_pages, 4) || !aligned(free_count, 4)) return PA_ERR_ALIGNMENT;
+  char* ws = static_cast<char*>(workspace(kFixedBytes, static_cast<cudaStream_t>(stream), &st));
+  if (!ws) return st;
+  ResizeParams p;
+  std::memset(&p, 0, sizeof p);
+  p.block_table = block_table;
+  p.row_ids = row_ids;
+  p.kv_lens = kv_lens;
+  p.deltas = deltas;
+  p.free_pages = free_pages;
+  p.free_count = free_count;
+  p.err = reinterpret_cast<int*>(ws + kErrOffset);
+  p.batch = batch;
+  p.rows = rows;
+  p.max_pages = max_pages;
+  p.table_stride = table_stride;
+  p.log2_page = log2_of(page_size);
+  p.free_size = free_size;
+  prof_mark(static_cast<cudaStream_t>(stream), true);
+  const cudaError_t e = launch_resize_tables(p, static_cast<cudaStream_t>(stream));
+  prof_mark(static_cast<cudaStream_t>(stream), false);
+  if (e != cudaSuccess) return PA_ERR_CUDA;
+  std::snprintf(g_variant, sizeof g_variant, "resize_tables");
+  return PA_OK;
+}
+
+int paged_attn_build_tables(const int32_t* block_table, int rows, int max_pages, int table_stride,
+                            const int32_t* row_ids, const int32_t* kv_lens, const int32_t* new_counts, int batch,
+                            int page_size, int num_pages, int32_t* kv_indptr, int32_t* kv_indices, int max_indices,
+                            int32_t* kv_last_page_len, int32_t* new_indptr, int64_t* slot_map, int32_t* positions,
+                            int num_tokens, void* stream) {
+  int st = check_tables(block_table, rows, max_pages, table_stride, row_ids, kv_lens, new_counts, batch, page_size);
+  if (st != PA_OK) return st;
+  if (num_pages < 1 || max_indices < 0 || num_tokens < 0) return PA_ERR_INVALID_ARG;
+  if (!kv_indptr || !new_indptr) return PA_ERR_INVALID_ARG;
+  if (batch > 0 && (!kv_last_page_len || (max_indices > 0 && !kv_indices))) return PA_ERR_INVALID_ARG;
+  if (!aligned(kv_indptr, 4) || !aligned(kv_indices, 4) || !aligned(kv_last_page_len, 4) ||
+      !aligned(new_indptr, 4) || !aligned(slot_map, 8) || !aligned(positions, 4))
+    return PA_ERR_ALIGNMENT;
+  int smem_optin = 0;
+  const int sms = device_sms(&smem_optin);
+  if (sms <= 0) return PA_ERR_CUDA;
+  char* ws = static_cast<char*>(workspace(kFixedBytes, static_cast<cudaStream_t>(stream), &st));
+  if (!ws) return st;
+  BuildParams p;
+  std::memset(&p, 0, sizeof p);
+  p.block_table = block_table;
+  p.row_ids = row_ids;
+  p.kv_lens = kv_lens;
+  p.new_counts = new_counts;
+  p.kv_indptr = kv_indptr;
+  p.kv_indices = kv_indices;
+  p.kv_last_page_len = kv_last_page_len;
+  p.new_indptr = new_indptr;
+  p.slot_map = slot_map;
+  p.positions = positions;
+  p.err = reinterpret_cast<int*>(ws + kErrOffset);
+  p.batch = batch;
+  p.rows = rows;
+  p.max_pages = max_pages;
+  p.table_stride = table_stride;
+  p.log2_page = log2_of(page_size);
+  p.num_pages = num_pages;
+  p.max_indices = max_indices;
+  p.num_tokens = num_tokens;
+  prof_mark(static_cast<cudaStream_t>(stream), true);
+  const cudaError_t e = launch_build_tables(p, sms, static_cast<cudaStream_t>(stream));
+  prof_mark(static_cast<cudaStream_t>(stream), false);
+  if (e != cudaSuccess) return PA_ERR_CUDA;
+  std::snprintf(g_variant, sizeof g_variant, "build_tables");
   return PA_OK;
 }
 
@@ -910,8 +1090,10 @@ extern "C" int paged_attn_decode_noalloc(const void* q, const void* kv_cache, co
   p.kv_indptr = kv_indptr;
   p.kv_indices = kv_indices;
   p.kv_last_page_len = kv_last_page_len;
-  p.k_scale = kv_dtype != PA_KV_BF16 ? kv_scales->k_scale : nullptr;
-  p.v_scale = kv_dtype != PA_KV_BF16 ? kv_scales->v_scale : nullptr;
+  const bool per_tensor = kv_dtype == PA_KV_FP8_E4M3 || kv_dtype == PA_KV_NVFP4;
+  p.k_scale = per_tensor ? kv_scales->k_scale : nullptr;
+  p.v_scale = per_tensor ? kv_scales->v_scale : nullptr;
+  p.bs = block_scales(kv_dtype, kv_scales, page_size);
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
   p.err = reinterpret_cast<int*>(ws + kErrOffset);
@@ -943,11 +1125,12 @@ extern "C" int paged_attn_decode_noalloc(const void* q, const void* kv_cache, co
   prof_mark(L.stream, true);
   if (kv_dtype == PA_KV_BF16) e = launch_decode_bf16(head_dim_qk, head_dim_vo, hp, L, &name);
   else if (kv_dtype == PA_KV_FP8_E4M3) e = launch_decode_fp8(head_dim_qk, head_dim_vo, hp, L, &name);
+  else if (kv_dtype == PA_KV_INT8_BLOCK) e = launch_decode_int8b(head_dim_qk, head_dim_vo, hp, L, &name);
+  else if (kv_dtype == PA_KV_FP8_BLOCK) e = launch_decode_fp8b(head_dim_qk, head_dim_vo, hp, L, &name);
   else e = launch_decode_nvfp4(head_dim_qk, head_dim_vo, hp, L, &name);
   prof_mark(L.stream, false);
   if (e != cudaSuccess) return PA_ERR_CUDA;
   if (!direct && launch_decode_merge(head_dim_vo, p, L.grid, L.stream) != cudaSuccess) return PA_ERR_CUDA;
-  static const char* kv_names[3] = {"bf16", "fp8", "nvfp4"};
   std::snprintf(g_variant, sizeof g_variant, "%s_%s%s_noalloc", name, kv_names[kv_dtype], direct ? "_direct" : "");
   return PA_OK;
 }

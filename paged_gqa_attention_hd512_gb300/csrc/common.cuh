@@ -194,6 +194,16 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two_codes_in_low16)
       : "r"(two_codes_in_low16));
   return r;
 }
+// Bytes A and B (0..3) of r, int8 codes with their top bit flipped (code + 128), as an f16
+// pair of the codes (A in the low half); exact: byte b under 0x64 is the f16 1024 + b.
+template <int A, int B>
+__device__ __forceinline__ uint32_t i8_biased_pair_f16x2(uint32_t r) {
+  uint32_t v;
+  asm("prmt.b32 %0, %1, 0x64646464, %2;" : "=r"(v) : "r"(r), "n"(0x4040 | A | (B << 8)));
+  const uint32_t bias = 0x64806480u;  // 1152 = 1024 + 128
+  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&bias));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
 // Four bytes of packed e2m1 pairs -> four f16x2 (byte k -> out[k]; low nibble -> low half).
 __device__ __forceinline__ void e2m1x8_to_f16x2x4(uint32_t src, uint32_t* out) {
   asm volatile(

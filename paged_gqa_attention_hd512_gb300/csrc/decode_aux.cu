@@ -28,6 +28,8 @@ cudaError_t launch_decode_merge(int dvo, const DecodeParams& p, int sms, cudaStr
 int decode_smem_bytes(int kvt, int dqk, int dvo, int hp) {
   if (kvt == KV_BF16) return smem_of<KV_BF16>(dqk, dvo, hp);
   if (kvt == KV_FP8) return smem_of<KV_FP8>(dqk, dvo, hp);
+  if (kvt == KV_INT8B) return smem_of<KV_INT8B>(dqk, dvo, hp);
+  if (kvt == KV_FP8B) return smem_of<KV_FP8B>(dqk, dvo, hp);
   return smem_of<KV_NVFP4>(dqk, dvo, hp);
 }
 

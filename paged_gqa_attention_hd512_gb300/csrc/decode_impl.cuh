@@ -22,7 +22,9 @@ namespace pa {
 // ----------------------------------------------------------------------------- config
 template <int KVT, int DQK, int DVO>
 struct DecodeCfg {
-  static constexpr int X2 = KVT == KV_BF16 ? 4 : (KVT == KV_FP8 ? 2 : 1);  // 2 * bytes/elem
+  static constexpr bool BLK = kv_block_scaled(KVT);  // 8-bit codes, a scale per block of tokens
+  static constexpr bool B8 = KVT == KV_FP8 || BLK;   // one byte per element
+  static constexpr int X2 = KVT == KV_BF16 ? 4 : (B8 ? 2 : 1);  // 2 * bytes/elem
   static constexpr int K_ROW = DQK * X2 / 2;  // bytes of one K row
   static constexpr int V_ROW = DVO * X2 / 2;
   static constexpr int T = (KVT == KV_BF16 && DQK == 512) ? 32 : 64;  // tokens per tile
@@ -44,6 +46,10 @@ struct DecodeCfg {
   static constexpr int KSW = DQW / 16;       // k-steps of QK^T per warp
   static constexpr int DVW = DVO / 8;        // output columns per warp
   static constexpr int MTV = DVW / 16;       // m-tiles of (PV)^T per warp
+  // warps 0-7 consume, 8 produces, 9 (block-scaled codes) brings each tile's scales
+  static constexpr int THREADS = BLK ? 320 : 288;
+  // floats of a stage's scales: K [T], V [T], the largest V scale of the tile
+  static constexpr int SC_STAGE = BLK ? 2 * T + 4 : 0;
   static_assert(K_ROW % 128 == 0 && V_ROW % 128 == 0, "rows must be whole 128-byte segments");
   static_assert(NS >= 2, "ring too shallow");
 };
@@ -59,7 +65,8 @@ struct DecodeSmem {
   static constexpr int OFF_ALPHA = OFF_P + PS;
   static constexpr int OFF_ML = OFF_ALPHA + HP * 4;
   static constexpr int OFF_QMAX = OFF_ML + HP * 8;
-  static constexpr int OFF_BAR = (OFF_QMAX + 8 * 4 + 7) / 8 * 8;
+  static constexpr int OFF_SC = (OFF_QMAX + 8 * 4 + 15) / 16 * 16;
+  static constexpr int OFF_BAR = OFF_SC + C::NS * C::SC_STAGE * 4;
   static constexpr int BYTES = OFF_BAR + 2 * C::NS * 8;
   static constexpr int ALLOC = BYTES + 1024;  // slack to align the base to 1024 bytes
 };
@@ -347,7 +354,7 @@ template <int KVT>
 __device__ __forceinline__ int q_col(int base, int ks, int half, int tig) {
   if constexpr (KVT == KV_BF16) {
     return base + 16 * ks + 2 * tig + 8 * half;
-  } else if constexpr (KVT == KV_FP8) {
+  } else if constexpr (KVT == KV_FP8 || kv_block_scaled(KVT)) {
     return base + 32 * (ks >> 1) + 16 * (ks & 1) + 4 * tig + 2 * half;
   } else {
     return base + 64 * (ks >> 2) + 32 * ((ks >> 1) & 1) + 8 * tig + 4 * (ks & 1) + 2 * half;
@@ -360,7 +367,7 @@ template <int KVT>
 __device__ __forceinline__ int o_col(int dv0, int i, int half, int gid) {
   if constexpr (KVT == KV_BF16) {
     return dv0 + 16 * i + gid + 8 * half;
-  } else if constexpr (KVT == KV_FP8) {
+  } else if constexpr (KVT == KV_FP8 || kv_block_scaled(KVT)) {
     return dv0 + 32 * (i >> 1) + 16 * (i & 1) + 2 * gid + half;
   } else {
     return dv0 + 64 * (i >> 2) + 32 * ((i >> 1) & 1) + 4 * gid + 2 * (i & 1) + half;
@@ -381,8 +388,17 @@ __device__ __forceinline__ void fp4_vt_pairs(uint32_t r, uint32_t* f) {
   e2m1x8_to_f16x2x4(ta | (tb << 4), f);        // byte e = (t_a, t_b) at column e
 }
 
+// Bytes A and B (0..3) of r as an f16 pair, A in the low half; exact for both code types.
+template <int KVT, int A, int B>
+__device__ __forceinline__ uint32_t b8_pair_f16x2(uint32_t r) {
+  if constexpr (KVT == KV_INT8B) return i8_biased_pair_f16x2<A, B>(r ^ 0x80808080u);
+  else if constexpr (A == 0 && B == 1) return e4m3x2_to_f16x2(r & 0xFFFFu);
+  else if constexpr (A == 2 && B == 3) return e4m3x2_to_f16x2(r >> 16);
+  else return e4m3x2_to_f16x2(prmt(r, 0, A | (B << 4)));
+}
+
 template <int KVT, int DQK, int DVO, int HP>
-__global__ void __launch_bounds__(288, 1)
+__global__ void __launch_bounds__(DecodeCfg<KVT, DQK, DVO>::THREADS, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const __grid_constant__ CUtensorMap tm_sfk,
                   const __grid_constant__ CUtensorMap tm_sfv, const DecodeParams p) {
@@ -404,7 +420,7 @@ __global__ void __launch_bounds__(288, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], C::BLK ? 2 : 1);  // the producer, and the warp that brings the scales
       mbar_init(&empty[s], 8);
     }
     fence_mbar_init();
@@ -459,6 +475,77 @@ __global__ void __launch_bounds__(288, 1)
     return;
   }
 
+  if constexpr (C::BLK) {
+    if (warp == 9) {
+      // ---------------------------------------------------------------- block scales
+      // The K and V scale of each token of a tile into the tile's stage (0 past the end of
+      // the sequence), two tokens per lane, and the tile's largest V scale.  Page ids are
+      // fetched two tiles ahead and scales one tile ahead of the wait for the stage, so the
+      // two dependent loads behind a scale are off the consumers' path.
+      float* sc0 = reinterpret_cast<float*>(smem + L::OFF_SC);
+      const int lps = 31 - __clz(ps);
+      uint32_t g = 0;
+      for (int it = blockIdx.x; it < n_items; it += gridDim.x) {
+        const DecodeChunk ch = decode_item_chunk(p, it);
+        const int kvh = it % p.Hkv;
+        const int ip0 = p.kv_indptr[ch.b];
+        const int np = p.kv_indptr[ch.b + 1] - ip0;
+        const int kv_len = (np - 1) * ps + p.kv_last_page_len[ch.b];
+        const int tok_end = min(ch.page_end * ps, kv_len);
+        int page[T / 32];
+        float ks[T / 32], vs[T / 32];
+        auto load_pages = [&](int tok0) {
+#pragma unroll
+          for (int k = 0; k < T / 32; ++k) {
+            const int tok = tok0 + lane + 32 * k;
+            page[k] = tok < tok_end ? __ldg(p.kv_indices + ip0 + (tok >> lps)) : -1;
+          }
+        };
+        auto load_scales = [&](int tok0) {
+#pragma unroll
+          for (int k = 0; k < T / 32; ++k) {
+            ks[k] = vs[k] = 0.f;
+            if (page[k] >= 0) {
+              const int blk = ((tok0 + lane + 32 * k) & (ps - 1)) >> p.bs.log2_tokens;
+              const float* src = p.bs.s + ((size_t)page[k] * 2 * p.Hkv + kvh) * p.bs.per_head + blk;
+              ks[k] = __ldg(src);
+              vs[k] = __ldg(src + (size_t)p.Hkv * p.bs.per_head);
+            }
+          }
+        };
+        const int t_begin = ch.page_begin * ps;
+        load_pages(t_begin);
+        load_scales(t_begin);
+        load_pages(t_begin + T);
+        for (int tok0 = t_begin; tok0 < tok_end; tok0 += T, ++g) {
+          const int s = g % NS;
+          float k_now[T / 32], v_now[T / 32];
+          uint32_t vmax = 0;
+#pragma unroll
+          for (int k = 0; k < T / 32; ++k) {
+            k_now[k] = ks[k];
+            v_now[k] = vs[k];
+            vmax = max(vmax, __float_as_uint(fabsf(vs[k])));
+          }
+          load_scales(tok0 + T);
+          load_pages(tok0 + 2 * T);
+          vmax = __reduce_max_sync(0xffffffffu, vmax);
+          mbar_wait(&empty[s], ((g / NS) & 1) ^ 1, p.err, SITE_DEC_EMPTY);
+          float* sc = sc0 + s * C::SC_STAGE;
+#pragma unroll
+          for (int k = 0; k < T / 32; ++k) {
+            sc[lane + 32 * k] = k_now[k];
+            sc[T + lane + 32 * k] = v_now[k];
+          }
+          if (lane == 0) sc[2 * T] = __uint_as_float(vmax);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[s]);
+        }
+      }
+      return;
+    }
+  }
+
   // -------------------------------------------------------------------- consumers
   const int cw = warp;  // 0..7
   const int gid = lane >> 2, tig = lane & 3;
@@ -469,8 +556,8 @@ __global__ void __launch_bounds__(288, 1)
   const int swz = p.swz;
   const int lbr = p.box_shift;
   const int gsz = p.group;
-  const float kscale = BF ? 1.f : __ldg(p.k_scale);
-  const float vscale = BF ? 1.f : __ldg(p.v_scale);
+  const float kscale = BF || C::BLK ? 1.f : __ldg(p.k_scale);
+  float vscale = BF || C::BLK ? 1.f : __ldg(p.v_scale);
   constexpr int PST = L::P_STRIDE;
   uint32_t g = 0;
 
@@ -555,6 +642,10 @@ __global__ void __launch_bounds__(288, 1)
       l_run[j] = 0.f;
     }
 
+    // block scales: P is written as p * vs * 2^(140 - veb), veb the largest biased exponent
+    // of the item's V scales so far (at least 14): at most 2^14 in f16, and full f16
+    // precision down to 2^-28 of the largest; O is rescaled where veb grows
+    int veb = 14;
     const int n_tiles = (tok_end - tok_begin + T - 1) / T;
     for (int ti = 0; ti < n_tiles; ++ti, ++g) {
       const int s = g % NS;
@@ -602,7 +693,7 @@ __global__ void __launch_bounds__(288, 1)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) mma16816<true>(sacc[nt], a0, a1, a2, a3, qf[ks][nt][0], qf[ks][nt][1]);
         }
-      } else if constexpr (KVT == KV_FP8) {
+      } else if constexpr (C::B8) {
 #pragma unroll
         for (int kg = 0; kg < C::KSW / 2; ++kg) {
           uint32_t R[4];
@@ -612,8 +703,8 @@ __global__ void __launch_bounds__(288, 1)
 #pragma unroll
           for (int sub = 0; sub < 2; ++sub) {
             const uint32_t ra = R[2 * sub], rb = R[2 * sub + 1];
-            const uint32_t a0 = e4m3x2_to_f16x2(ra & 0xFFFFu), a2 = e4m3x2_to_f16x2(ra >> 16);
-            const uint32_t a1 = e4m3x2_to_f16x2(rb & 0xFFFFu), a3 = e4m3x2_to_f16x2(rb >> 16);
+            const uint32_t a0 = b8_pair_f16x2<KVT, 0, 1>(ra), a2 = b8_pair_f16x2<KVT, 2, 3>(ra);
+            const uint32_t a1 = b8_pair_f16x2<KVT, 0, 1>(rb), a3 = b8_pair_f16x2<KVT, 2, 3>(rb);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
               mma16816<false>(sacc[nt], a0, a1, a2, a3, qf[2 * kg + sub][nt][0], qf[2 * kg + sub][nt][1]);
@@ -665,6 +756,20 @@ __global__ void __launch_bounds__(288, 1)
       named_bar_sync(1, 256);
 
       // ---- online softmax: warp cw owns heads cw + 8j, lanes own tokens
+      float vfac = 1.f;  // block scales: the factor of O for a larger veb
+      float kst[C::BLK ? T / 32 : 1], vst[C::BLK ? T / 32 : 1];
+      if constexpr (C::BLK) {
+        const float* sc = reinterpret_cast<const float*>(smem + L::OFF_SC) + s * C::SC_STAGE;
+        const int eb = max(veb, (int)(__float_as_uint(sc[2 * T]) >> 23));
+        if (eb > veb) vfac = eb - veb < 127 ? __uint_as_float((uint32_t)(127 + veb - eb) << 23) : 0.f;
+        veb = eb;
+        const float f = __uint_as_float((uint32_t)(267 - eb) << 23);
+#pragma unroll
+        for (int k = 0; k < T / 32; ++k) {
+          kst[k] = sc[lane + 32 * k] * sm_log2;
+          vst[k] = sc[T + lane + 32 * k] * f;
+        }
+      }
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         const int h = cw + 8 * j;
@@ -677,7 +782,8 @@ __global__ void __launch_bounds__(288, 1)
 #pragma unroll
           for (int q = 0; q < C::NDQ; ++q) sv += sred[(q * HP + h) * (T + 4) + t];
           const bool ok = (t < n_valid) && (tok0 + t >= win_lo);
-          x[k] = ok ? sv * sm_log2 : -INFINITY;
+          if constexpr (C::BLK) x[k] = ok ? sv * kst[k] : -INFINITY;
+          else x[k] = ok ? sv * sm_log2 : -INFINITY;
           tmax = fmaxf(tmax, x[k]);
         }
 #pragma unroll
@@ -691,6 +797,7 @@ __global__ void __launch_bounds__(288, 1)
           sum += pv;
           uint16_t bits;
           if constexpr (BF) bits = __bfloat16_as_ushort(__float2bfloat16_rn(pv));
+          else if constexpr (C::BLK) bits = __half_as_ushort(__float2half_rn(pv * vst[k]));
           else bits = __half_as_ushort(__float2half_rn(pv));
           Ps[h * PST + lane + 32 * k] = bits;
         }
@@ -700,7 +807,7 @@ __global__ void __launch_bounds__(288, 1)
         l_run[j] = l_run[j] * alpha + sum;
         m_run[j] = m_new;
         if (lane == 0) {
-          alpha_s[h] = alpha;
+          alpha_s[h] = C::BLK ? alpha * vfac : alpha;
           ml_s[h] = make_float2(m_new, l_run[j]);
         }
       }
@@ -738,7 +845,7 @@ __global__ void __launch_bounds__(288, 1)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma16816<true>(o[i][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
           }
-        } else if constexpr (KVT == KV_FP8) {
+        } else if constexpr (C::B8) {
 #pragma unroll
           for (int ip = 0; ip < C::MTV / 2; ++ip) {
             uint32_t R[4];
@@ -748,8 +855,8 @@ __global__ void __launch_bounds__(288, 1)
 #pragma unroll
             for (int sub = 0; sub < 2; ++sub) {
               const uint32_t ra = R[2 * sub], rb = R[2 * sub + 1];
-              const uint32_t a0 = e4m3x2_to_f16x2(prmt(ra, 0, 0x20)), a1 = e4m3x2_to_f16x2(prmt(ra, 0, 0x31));
-              const uint32_t a2 = e4m3x2_to_f16x2(prmt(rb, 0, 0x20)), a3 = e4m3x2_to_f16x2(prmt(rb, 0, 0x31));
+              const uint32_t a0 = b8_pair_f16x2<KVT, 0, 2>(ra), a1 = b8_pair_f16x2<KVT, 1, 3>(ra);
+              const uint32_t a2 = b8_pair_f16x2<KVT, 0, 2>(rb), a3 = b8_pair_f16x2<KVT, 1, 3>(rb);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
                 mma16816<false>(o[2 * ip + sub][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
@@ -798,6 +905,7 @@ __global__ void __launch_bounds__(288, 1)
     const int2 si = p.direct ? make_int2(0, 1) : p.seq_info[b];
     const bool direct = (si.y == 1);
     const bool keys = n_tiles > 0;
+    if constexpr (C::BLK) vscale = __uint_as_float((uint32_t)(veb - 13) << 23);  // 2^(veb - 140)
     const size_t prow = (size_t)(si.x + ch.split);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)

@@ -1,6 +1,6 @@
 // decode_inst.cuh -- instantiates the decode kernel for one KV dtype.  Included by
-// decode_bf16.cu / decode_fp8.cu / decode_nvfp4.cu with PA_KVT defined, so that the three
-// dtypes compile as separate translation units in parallel.
+// decode_bf16.cu / decode_fp8.cu / decode_nvfp4.cu / decode_int8b.cu / decode_fp8b.cu, so that the dtypes
+// compile as separate translation units in parallel.
 #pragma once
 
 #include "decode_impl.cuh"
@@ -15,7 +15,7 @@ static cudaError_t run_decode(const DecodeLaunch& L) {
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sm::ALLOC);
   if (e != cudaSuccess) return e;
   // a programmatic dependent of the planner
-  return launch_pdl(kern, dim3(L.grid), dim3(288), Sm::ALLOC, L.stream, 1, L.tk, L.tv, L.tsfk, L.tsfv, L.p);
+  return launch_pdl(kern, dim3(L.grid), dim3(DecodeCfg<KVT, DQK, DVO>::THREADS), Sm::ALLOC, L.stream, 1, L.tk, L.tv, L.tsfk, L.tsfv, L.p);
 }
 
 template <int KVT>

@@ -5,7 +5,17 @@
 
 namespace pa {
 
-enum { KV_BF16 = 0, KV_FP8 = 1, KV_NVFP4 = 2 };
+// (KV_INT8B, KV_FP8B: int8 / e4m3 codes with one fp32 scale per block of tokens and kv head)
+enum { KV_BF16 = 0, KV_FP8 = 1, KV_NVFP4 = 2, KV_INT8B = 3, KV_FP8B = 4 };
+constexpr bool kv_block_scaled(int kvt) { return kvt == KV_INT8B || kvt == KV_FP8B; }
+
+// Block scales of a KV_INT8B / KV_FP8B cache: fp32 [num_pages][2][Hkv][page_size >> log2_tokens]
+// (0: K, 1: V), a block being 2^log2_tokens consecutive slots of a page.
+struct BlockScales {
+  const float* s;
+  int log2_tokens;
+  int per_head;  // blocks of one page and head: page_size >> log2_tokens
+};
 
 // Wait-site ids recorded in the error word when a bounded wait gives up.
 enum {
@@ -21,7 +31,10 @@ enum {
   SITE_PRE_DEQ = 208,
   SITE_PRE_STG = 209,
   SITE_PRE_SF = 210,
+  SITE_PRE_ALIGN = 211,  // prefill: the shared memory window is not 1024-byte aligned
   SITE_APPEND_POS = 301,  // append: more new tokens than the sequence holds, or a page id out of range
+  SITE_RESIZE = 401,  // table resize: a bad row or length, no room in a row or no free page
+  SITE_BUILD = 402,   // table build: a bad row, length or page id, or more entries than the outputs hold
 };
 
 // Decode work list entry: one page-aligned chunk of one sequence.
@@ -59,6 +72,7 @@ struct DecodeParams {
   // (no planner, no split, no merge: problems whose every item fits one CTA's round)
   int direct;
   float sm_scale;
+  BlockScales bs;  // KV_INT8B / KV_FP8B
 };
 
 // Prefill work item: one tile of query rows (positions x heads of one kv head).
@@ -128,6 +142,7 @@ struct PrefillParams {
   int out_v8;  // out is 32-byte aligned: the epilogue writes whole 32-byte sectors
   int swz;
   float sm_scale;
+  BlockScales bs;  // KV_INT8B / KV_FP8B (also when the kernel reads their 16-bit copy)
 };
 
 // Pages -> bf16 copy for the prefill (see prefill_dequant.cuh): FP8 / NVFP4 pages
@@ -157,6 +172,50 @@ struct AppendParams {
   uint8_t* sf;           // NVFP4 block-scale pool (same page indexing)
   int* err;
   int batch, total_new, num_pages, Hkv, d_qk, d_vo, page_size;
+};
+
+// New tokens' K / V (bf16) -> a paged cache of 8-bit codes with block scales (append_block.cu)
+struct AppendBlockParams {
+  const uint16_t* k_new;  // bf16 [total_new, Hkv, d_qk]
+  const uint16_t* v_new;  // bf16 [total_new, Hkv, d_vo]
+  const int32_t* append_indptr;  // [batch + 1]
+  const int32_t* kv_indptr;
+  const int32_t* kv_indices;
+  const int32_t* kv_last_page_len;
+  uint8_t* cache;
+  float* scales;    // [num_pages][2][Hkv][per_head]
+  int* err;
+  int log2_tokens;  // tokens of a block
+  int per_head;     // blocks of a page and head
+  int batch, total_new, num_pages, Hkv, d_qk, d_vo, page_size;
+};
+
+// Requests that grow or shrink (tables.cu)
+struct ResizeParams {
+  int32_t* block_table;    // [rows][table_stride], the first max_pages entries of a row in use
+  const int32_t* row_ids;  // [batch] or nullptr (row b)
+  int32_t* kv_lens;        // [rows]
+  const int32_t* deltas;   // [batch]
+  int32_t* free_pages;     // [free_size]
+  int32_t* free_count;
+  int* err;
+  int batch, rows, max_pages, table_stride, log2_page, free_size;
+};
+
+// Block table and lengths -> CSR page lists, new-token offsets, slots, positions (tables.cu)
+struct BuildParams {
+  const int32_t* block_table;
+  const int32_t* row_ids;     // [batch] or nullptr (row b)
+  const int32_t* kv_lens;     // [rows]
+  const int32_t* new_counts;  // [batch]
+  int32_t* kv_indptr;         // [batch + 1]
+  int32_t* kv_indices;        // [max_indices]
+  int32_t* kv_last_page_len;  // [batch]
+  int32_t* new_indptr;        // [batch + 1]
+  int64_t* slot_map;          // [num_tokens] or nullptr
+  int32_t* positions;         // [num_tokens] or nullptr
+  int* err;
+  int batch, rows, max_pages, table_stride, log2_page, num_pages, max_indices, num_tokens;
 };
 
 }  // namespace pa

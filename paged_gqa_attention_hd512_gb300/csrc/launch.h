@@ -73,6 +73,9 @@ cudaError_t launch_pdl(Kern kern, dim3 grid, dim3 block, size_t smem, cudaStream
 cudaError_t launch_decode_bf16(int dqk, int dvo, int hp, const DecodeLaunch& L, const char** variant);
 cudaError_t launch_decode_fp8(int dqk, int dvo, int hp, const DecodeLaunch& L, const char** variant);
 cudaError_t launch_decode_nvfp4(int dqk, int dvo, int hp, const DecodeLaunch& L, const char** variant);
+// 8-bit codes with block scales (kvt KV_INT8B or KV_FP8B)
+cudaError_t launch_decode_int8b(int dqk, int dvo, int hp, const DecodeLaunch& L, const char** variant);
+cudaError_t launch_decode_fp8b(int dqk, int dvo, int hp, const DecodeLaunch& L, const char** variant);
 cudaError_t launch_decode_plan(const DecodeParams& p, cudaStream_t s);
 cudaError_t launch_decode_merge(int dvo, const DecodeParams& p, int sms, cudaStream_t s);
 // Shared memory (bytes) the decode kernel of this shape needs.
@@ -89,9 +92,17 @@ cudaError_t launch_prefill_prep(int kvt, int dqk, int dvo, int copy, const Prefi
 // Split KV: merges the partial slots the plan listed (hdr[1] entries) into the output.
 cudaError_t launch_prefill_merge(int dvo, const PrefillParams& p, int grid, cudaStream_t s);
 int prefill_smem_bytes(int kvt, int dqk, int dvo);
+// The same for codes with block scales: kvt KV_INT8B / KV_FP8B converted in the kernel, or
+// KV_BF16 for their 16-bit copy.
+cudaError_t launch_prefill_block(int kvt, int dqk, int dvo, const PrefillLaunch& L, const char** variant);
+int prefill_block_smem_bytes(int kvt, int dqk, int dvo);
 // Two-CTA clusters of the bf16 prefill kernel that fit on the device at once.
 int prefill_pair_clusters(int dqk, int dvo);
 // New tokens' bf16 K / V -> the paged cache in its element type (quantise-on-write).
 cudaError_t launch_append_kv(int kvt, const AppendParams& p, int sms, cudaStream_t s);
+// The same into 8-bit codes with block scales (kvt KV_INT8B or KV_FP8B).
+cudaError_t launch_append_block(int kvt, const AppendBlockParams& p, cudaStream_t s);
+cudaError_t launch_resize_tables(const ResizeParams& p, cudaStream_t s);
+cudaError_t launch_build_tables(const BuildParams& p, int sms, cudaStream_t s);
 
 }  // namespace pa

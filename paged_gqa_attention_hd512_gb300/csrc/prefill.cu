@@ -43,6 +43,10 @@ cudaError_t launch_prefill_prep(int kvt, int dqk, int dvo, int copy, const Prefi
   const bool pad = copy == 2;
   if (kvt == KV_BF16) return pad ? run_prep<KV_BF16, true>(dqk, dvo, grid, p, d, s) : cudaErrorInvalidValue;
   if (kvt == KV_FP8) return pad ? run_prep<KV_FP8, true>(dqk, dvo, grid, p, d, s) : run_prep<KV_FP8, false>(dqk, dvo, grid, p, d, s);
+  if (kvt == KV_INT8B)
+    return pad ? run_prep<KV_INT8B, true>(dqk, dvo, grid, p, d, s) : run_prep<KV_INT8B, false>(dqk, dvo, grid, p, d, s);
+  if (kvt == KV_FP8B)
+    return pad ? run_prep<KV_FP8B, true>(dqk, dvo, grid, p, d, s) : run_prep<KV_FP8B, false>(dqk, dvo, grid, p, d, s);
   if (kvt == KV_NVFP4)
     return pad ? run_prep<KV_NVFP4, true>(dqk, dvo, grid, p, d, s) : run_prep<KV_NVFP4, false>(dqk, dvo, grid, p, d, s);
   return cudaErrorInvalidValue;

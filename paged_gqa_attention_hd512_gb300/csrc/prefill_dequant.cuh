@@ -12,6 +12,9 @@
 // (qk=512/vo=256) for Gemma-4 on SM120/121", NVFP4 split-KV correctness: scales of 16
 // elements along head_dim of one token).
 //
+// int8 and e4m3 codes with a scale per block of tokens are copied as the codes' values, K in
+// bf16 and V in f16 (both exact); the prefill kernel applies the scales to S and P.
+//
 // Pages of fewer than 8 tokens cannot be loaded as the 128B-swizzled boxes of whole 8-row
 // atoms the MMAs read, so the copy gives each page 8 rows per kv head: its page_size
 // tokens, then zero rows; the kernel reads such a page as 8 rows and masks the padding.
@@ -62,14 +65,15 @@ __device__ __forceinline__ void prefill_dequant_body(const DequantParams& d, int
   const uint64_t stride = (uint64_t)nblk * blockDim.x;
   const size_t elems_out = (size_t)units * 16;                                 // values per copy page
   // bytes per caller page: 16 values per unit of 2, 1 or 1/2 bytes
-  const size_t in_page = (size_t)units_in * (KVT == KV_BF16 ? 32 : (KVT == KV_FP8 ? 16 : 8));
+  const size_t in_page = (size_t)units_in * (KVT == KV_BF16 ? 32 : (KVT == KV_NVFP4 ? 8 : 16));
+  const uint32_t k_units = (uint32_t)d.Hkv * rows_out * (DQK / 16);  // K units of a copy page (V units follow)
   const uint64_t pol_keep = l2_policy_evict_last();
   for (uint64_t g0 = (uint64_t)blk * blockDim.x + threadIdx.x; g0 < total; g0 += U * stride) {
     uint4 a8[U], b8[U];
     uint2 a4[U];
     uint32_t sb[U];
     size_t page[U], dst_elem[U];
-    bool zero[U];
+    bool zero[U], is_v[U];
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       const uint64_t g = g0 + k * stride;
@@ -79,6 +83,7 @@ __device__ __forceinline__ void prefill_dequant_body(const DequantParams& d, int
       page[k] = (size_t)__ldg(d.kv_indices + e);
       uint32_t us = u;
       zero[k] = false;
+      is_v[k] = u >= k_units;
       dst_elem[k] = (size_t)u * 16;
       if constexpr (PAD) {
         int r;
@@ -92,7 +97,7 @@ __device__ __forceinline__ void prefill_dequant_body(const DequantParams& d, int
         const uint4* src = reinterpret_cast<const uint4*>(d.cache + page[k] * in_page) + 2 * (size_t)us;
         a8[k] = __ldg(src);
         b8[k] = __ldg(src + 1);
-      } else if constexpr (KVT == KV_FP8) {
+      } else if constexpr (KVT != KV_NVFP4) {
         a8[k] = __ldg(reinterpret_cast<const uint4*>(d.cache + page[k] * in_page) + us);
       } else {
         a4[k] = __ldg(reinterpret_cast<const uint2*>(d.cache + page[k] * in_page) + us);
@@ -109,6 +114,22 @@ __device__ __forceinline__ void prefill_dequant_body(const DequantParams& d, int
       } else if constexpr (KVT == KV_BF16) {
         w[0] = a8[k].x, w[1] = a8[k].y, w[2] = a8[k].z, w[3] = a8[k].w;
         w[4] = b8[k].x, w[5] = b8[k].y, w[6] = b8[k].z, w[7] = b8[k].w;
+      } else if constexpr (kv_block_scaled(KVT)) {
+        const uint32_t in[4] = {a8[k].x, a8[k].y, a8[k].z, a8[k].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (KVT == KV_INT8B) {
+            w[2 * j] = i8_biased_pair_f16x2<0, 1>(in[j] ^ 0x80808080u);
+            w[2 * j + 1] = i8_biased_pair_f16x2<2, 3>(in[j] ^ 0x80808080u);
+          } else {
+            w[2 * j] = e4m3x2_to_f16x2(in[j] & 0xFFFFu);
+            w[2 * j + 1] = e4m3x2_to_f16x2(in[j] >> 16);
+          }
+        }
+        if (!is_v[k]) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) w[j] = f16x2_to_bf16x2(w[j]);
+        }
       } else if constexpr (KVT == KV_FP8) {
         const uint32_t in[4] = {a8[k].x, a8[k].y, a8[k].z, a8[k].w};
 #pragma unroll

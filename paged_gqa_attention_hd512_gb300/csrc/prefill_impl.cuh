@@ -38,8 +38,13 @@
 
 namespace pa {
 
-template <int DQK, int DVO, int KVT, bool PAIR_ = false>
+// SCALED_: 8-bit codes with a scale per block of tokens and kv head, either converted in the
+// kernel (KVT KV_INT8B / KV_FP8B) or read from their exact 16-bit copy (KVT KV_BF16: K in
+// bf16, V in f16).  The K scale of a key multiplies its column of S, the V scale its column
+// of P, so no K or V value is rounded.
+template <int DQK, int DVO, int KVT, bool PAIR_ = false, bool SCALED_ = kv_block_scaled(KVT)>
 struct PrefillCfg {
+  static constexpr bool SCALED = SCALED_;
   // PAIR: two CTAs (a cluster) share every MMA (tcgen05 cta_group::2, M = 256): each holds
   // its own 128 query rows and loads half of every K/V tile, so the pair reads each K/V
   // byte once instead of twice and each SM takes in half the K/V bytes per MMA cycle
@@ -62,6 +67,7 @@ struct PrefillCfg {
   static constexpr int Q_BYTES = NQB * HALF;
   static constexpr int SMEM_BUDGET = 232448 - 1024 - 512;
   static constexpr bool QUANT = KVT != KV_BF16;
+  static constexpr bool PV16 = QUANT || SCALED;  // P and V in f16 (otherwise bf16)
   // bf16 KV, one CTA per tile: a V chunk is 64 keys of the tile by the pass's 256 output
   // columns (four [64 keys][64 dims] 128B-swizzled blocks of 8 KB), so that P.V runs as
   // N = 256 MMAs (one per 16 keys, four per chunk): on this GPU an N = 128 MMA takes about
@@ -77,7 +83,7 @@ struct PrefillCfg {
   // into staging rings with TMA; the converters turn two staged halves into one slot of the
   // bf16 / f16 ring the MMAs read.  The staging rings hide the L2 latency, so the converted
   // ring only covers the conversion.
-  static constexpr int CW = KVT == KV_FP8 ? 64 : (KVT == KV_NVFP4 ? 32 : 0);  // packed bytes per key and half
+  static constexpr int CW = KVT == KV_FP8 || kv_block_scaled(KVT) ? 64 : (KVT == KV_NVFP4 ? 32 : 0);  // packed bytes per key and half
   static constexpr int STG_BYTES = N * CW;
   static constexpr int NQS = 2 * NQC, NVS = 2 * NVC;                         // staged halves per step
   static constexpr int SFW_K = DQK / 16, SFW_V = DVO / 16;                  // scale bytes per key
@@ -96,7 +102,10 @@ struct PrefillCfg {
   // the first pass rescaled O before that tile's PV (the second pass replays only those)
   static constexpr int MAX_RT = 64;
   static constexpr int OFF_RTAG = OFF_XCH + (SMW == 2 ? 1024 : 0);
-  static constexpr int OFF_BAR = OFF_RTAG + (NPASS == 2 ? MAX_RT * 4 : 0);
+  // SCALED: floats of the current KV tile: K scale [128], V scale x a power of two [128] per
+  // tile row, and the V scales' maximum (float bits) of each of four warps
+  static constexpr int OFF_SC = (OFF_RTAG + (NPASS == 2 ? MAX_RT * 4 : 0) + 15) / 16 * 16;
+  static constexpr int OFF_BAR = OFF_SC + (SCALED ? (128 + 128 + 4) * 4 : 0);
   // head_dim_vo 512 with P reuse: the second pass reads the first pass's P tiles into
   // NPS slots of the Q region (Q is not needed by then)
   static constexpr int NPS = NPASS == 2 ? Q_BYTES / CHUNK : 0;
@@ -111,7 +120,9 @@ struct PrefillCfg {
   static constexpr int NBAR = NB_FIXED + 2 * NSLOT + 2 * NSTG + 2 * NSF + 2 * NPS + NKC;
   static constexpr int QB_PER = NQB / NKC;  // 64-column Q blocks per K chunk
   static constexpr int BYTES = OFF_BAR + NBAR * 8 + 16;
-  static constexpr int ALLOC = BYTES + 1024;
+  // slack to align the base to 1024 bytes.  The scaled bf16-copy variant has no room for it:
+  // its window is declared 1024-byte aligned (the kernel checks that it is)
+  static constexpr int ALLOC = BYTES + (SCALED && !QUANT ? 0 : 1024);
   // TMEM columns: two S buffers of 128 keys (step j uses buffer j & 1; its P, 128 keys of
   // bf16 / f16, is written over the first 64 columns of the same buffer), O from 256
   static constexpr uint32_t TM_S = 0, TM_O = 256;
@@ -574,16 +585,21 @@ struct PrefillItemWalk {
 // tm_p (CTA pairs only): the P scratch as rows of 128 bytes, boxes of one 32 KB P tile
 // GEN: custom masks and small padded pages may occur (false: neither, their code is not
 // compiled in, which the plain causal / windowed calls run)
-template <int KVT, int DQK, int DVO, bool PAIR, bool GEN = true>
-__global__ void __launch_bounds__(PrefillCfg<DQK, DVO, KVT, PAIR>::THREADS, 1)
+// SC: the cache has block scales (see PrefillCfg)
+template <int KVT, int DQK, int DVO, bool PAIR, bool GEN = true, bool SC = kv_block_scaled(KVT)>
+__global__ void __launch_bounds__(PrefillCfg<DQK, DVO, KVT, PAIR, SC>::THREADS, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_sfk,
                    const __grid_constant__ CUtensorMap tm_sfv, const __grid_constant__ CUtensorMap tm_p,
                    const PrefillParams p) {
-  using C = PrefillCfg<DQK, DVO, KVT, PAIR>;
+  using C = PrefillCfg<DQK, DVO, KVT, PAIR, SC>;
   constexpr int NSLOT = C::NSLOT;
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  if (C::BYTES == C::ALLOC && smem != smem_raw) {
+    if (threadIdx.x == 0) record_error(p.err, SITE_PRE_ALIGN);
+    return;
+  }
   const uint32_t q_s = smem_u32(smem);
   const uint32_t ring = q_s + C::OFF_RING;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -1061,7 +1077,14 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DVO, KVT, PAIR>::THREADS, 1)
 #pragma unroll
         for (int jj = 0; jj < 8; ++jj) {  // 16-byte output chunk jj = elements 8jj .. 8jj+7
           uint32_t w[4];
-          if constexpr (KVT == KV_FP8) {
+          if constexpr (KVT == KV_INT8B) {
+            const uint4 a = raw[jj >> 1];
+            const uint32_t w0 = ((jj & 1) ? a.z : a.x) ^ 0x80808080u, w1 = ((jj & 1) ? a.w : a.y) ^ 0x80808080u;
+            w[0] = i8_biased_pair_f16x2<0, 1>(w0);
+            w[1] = i8_biased_pair_f16x2<2, 3>(w0);
+            w[2] = i8_biased_pair_f16x2<0, 1>(w1);
+            w[3] = i8_biased_pair_f16x2<2, 3>(w1);
+          } else if constexpr (KVT != KV_NVFP4) {
             const uint4 a = raw[jj >> 1];
             const uint32_t w0 = (jj & 1) ? a.z : a.x, w1 = (jj & 1) ? a.w : a.y;
             w[0] = e4m3x2_to_f16x2(w0 & 0xFFFFu);
@@ -1108,8 +1131,8 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DVO, KVT, PAIR>::THREADS, 1)
     constexpr uint32_t ID_QK = idesc_f16<true>(128 * C::CL, 128, false);
     // quantised KV: P and V in f16.  Pairs: one N = 256 MMA per 16 keys covers the pass's
     // output columns (128 from each CTA's V chunk)
-    constexpr uint32_t ID_PV = idesc_f16<!C::QUANT>(128 * C::CL, 128 * C::CL, true);
-    constexpr uint32_t ID_PV2 = idesc_f16<true>(128, 256, true);  // V by keys
+    constexpr uint32_t ID_PV = idesc_f16<!C::PV16>(128 * C::CL, 128 * C::CL, true);
+    constexpr uint32_t ID_PV2 = idesc_f16<!C::PV16>(128, 256, true);  // V by keys
     // MMA issue and commits: the pair forms (cta_group::2) in a CTA pair.  commit_both
     // signals the barrier in both CTAs, commit_here only in this (the first) CTA.
     auto mma_ss = [&](uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
@@ -1338,13 +1361,49 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DVO, KVT, PAIR>::THREADS, 1)
     constexpr int OCOL = C::DVP / C::SMW;
     const int ocol0 = wg * OCOL;
     // FP8 per-tensor / NVFP4 global K scale folds into the scores, the V scale into the output
-    // (also given for bf16 KV when it is the bf16 copy of FP8 / NVFP4 pages)
+    // (also given for bf16 KV when it is the bf16 copy of FP8 / NVFP4 pages; none with block
+    // scales, which are applied key by key)
     const float scale_log2 = p.sm_scale * 1.4426950408889634f * (p.k_scale ? __ldg(p.k_scale) : 1.f);
     // scores are scaled inside the exponent's FMA; a non-positive scale is applied up
     // front instead (the maximum of the raw scores is only the scaled maximum for scale > 0)
     const bool pos_scale = scale_log2 > 0.f;
     const float eff_scale = pos_scale ? scale_log2 : 1.f;
-    const float v_scale = p.v_scale ? __ldg(p.v_scale) : 1.f;
+    float v_scale = p.v_scale ? __ldg(p.v_scale) : 1.f;
+    // SCALED: this thread brings the scales of tile row sc_row: the K scale (first warpgroup,
+    // or the only one) and / or the V scale, from global memory through registers into
+    // shared memory, while the tiles before run:
+    //   raw scales of tile j + 1 are loaded before the wait for S of tile j (page id: one
+    //   tile earlier still);
+    //   between the two barriers of tile j's row-maximum exchange go K of tile j + 1 (K of
+    //   tile j was last read before the first of them), V of tile j (V of tile j - 1 was
+    //   last read before it too) and the warps' V maxima of tile j + 1 (those of tile j
+    //   were read at the start of tile j).
+    // V scales are written times 2^(132 - veb), veb the largest biased exponent of the V
+    // scales when O was last rescaled for it: P (at most 2^8, see the lazy rescale) times
+    // that stays below 2^15 in f16 while the tile's largest V scale is within 2 x of it.
+    const bool sc_k = !C::QUANT ? wg == 0 : true, sc_v = !C::QUANT ? wg == 1 : true;
+    float* ks_s = reinterpret_cast<float*>(smem + C::OFF_SC);
+    float* vs_s = ks_s + 128;
+    uint32_t* vm_s = reinterpret_cast<uint32_t*>(ks_s + 256);
+    constexpr int kMinVeb = 6;  // the power of two stays a normal float
+    int veb = kMinVeb;
+    auto sc_page = [&](const PrefillItemInfo& f, int tile) -> int {  // page of this thread's row, -1: no token
+      const int pg = tile * (128 / p.box_rows) + row / p.box_rows, slot = row % p.box_rows;
+      if (slot >= ps || pg >= f.np || pg * ps + slot >= f.kv_len) return -1;
+      return __ldg(p.kv_indices + f.ip0 + pg);
+    };
+    auto sc_load = [&](const PrefillItemInfo& f, int page, float& k, float& v) {
+      k = v = 0.f;
+      if (page < 0) return;
+      const float* s = p.bs.s + ((size_t)page * 2 * p.Hkv + f.kvh) * p.bs.per_head +
+                       ((row % p.box_rows) >> p.bs.log2_tokens);
+      if (sc_k) k = __ldg(s);
+      if (sc_v) v = __ldg(s + (size_t)p.Hkv * p.bs.per_head);
+    };
+    auto sc_warp_vmax = [&](float v) {
+      const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(v)));
+      if (sc_v && lane == 0) vm_s[quarter] = m;
+    };
     // TMEM halves as the MMA warp uses them: S at tm_s, the first pass's O at tm_o, a
     // second pass that reuses P at tm_s; swapped after every such item
     uint32_t flip = 0, tm_s = C::TM_S, tm_o = C::TM_O;
@@ -1420,8 +1479,33 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DVO, KVT, PAIR>::THREADS, 1)
         } else {
           m_used = -INFINITY;
           l = 0.f;
+          float v_cur = 0.f, k_nxt = 0.f, v_nxt = 0.f;  // raw scales of tiles jt, jt + 1
+          int pg_nxt = -1;                              // page of tile jt + 1
+          if constexpr (SC) {
+            // (every thread has passed the last exchange of the pass before: its K scales
+            // and V maxima are no longer read)
+            sc_load(f, sc_page(f, f.jlo), k_nxt, v_cur);
+            pg_nxt = f.nt > 1 ? sc_page(f, f.jlo + 1) : -1;
+            if (sc_k) ks_s[row] = k_nxt;
+            sc_warp_vmax(v_cur);
+            named_bar_sync(C::NB_SMX, 128 * C::SMW);
+          }
           for (int jt = 0; jt < f.nt; ++jt, ++sstep) {
             const uint32_t s_col = tm_s + 128 * (sstep & 1);
+            bool vgrow = false;
+            float vfac = 1.f;
+            if constexpr (SC) {
+              const int eb = (int)(max(max(vm_s[0], vm_s[1]), max(vm_s[2], vm_s[3])) >> 23);
+              if (jt == 0) {
+                veb = max(eb, kMinVeb);
+              } else if (eb > veb + 1) {
+                vgrow = true;
+                vfac = eb - veb < 127 ? __uint_as_float((uint32_t)(127 + veb - eb) << 23) : 0.f;
+                veb = eb;
+              }
+              sc_load(f, pg_nxt, k_nxt, v_nxt);
+              pg_nxt = jt + 2 < f.nt ? sc_page(f, f.jlo + jt + 2) : -1;
+            }
             mbar_wait<C::PAIR>(&s_full[sstep & 1], (sstep >> 1) & 1, p.err, SITE_PRE_S_FULL);
             __syncwarp();  // the tcgen05 loads below are warp-collective
             tc_fence_after();
@@ -1434,6 +1518,16 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DVO, KVT, PAIR>::THREADS, 1)
             // select on two compares (short-circuit forms compiled to per-element
             // branches).  The maximum is taken over the raw scores (the scale is positive,
             // or applied first when it is not); max and sum run as four chains.
+            if constexpr (SC) {
+#pragma unroll
+              for (int i = 0; i < NCOL; i += 4) {
+                const float4 k4 = *reinterpret_cast<const float4*>(ks_s + col0 + i);
+                sr[i] = __float_as_uint(__uint_as_float(sr[i]) * k4.x);
+                sr[i + 1] = __float_as_uint(__uint_as_float(sr[i + 1]) * k4.y);
+                sr[i + 2] = __float_as_uint(__uint_as_float(sr[i + 2]) * k4.z);
+                sr[i + 3] = __float_as_uint(__uint_as_float(sr[i + 3]) * k4.w);
+              }
+            }
             const int key0 = (f.jlo + jt) * 128 + col0;
             const int lo = klo - key0, hi = min(khi, f.kv_len - 1) - key0;
             float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -1497,8 +1591,20 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DVO, KVT, PAIR>::THREADS, 1)
               if (__all_sync(0xffffffffu, (lo <= 0) & (hi >= NCOL - 1) & all_ok)) plain_max();
               else mask_and_max(mw, true);
             }
-            const float mx =
-                combine(fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])), true) * eff_scale;
+            const float mx_own = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+            float mx;
+            if constexpr (SC) {
+              if (C::SMW == 2) xch[wg * 128 + row] = mx_own;
+              named_bar_sync(C::NB_SMX, 128 * C::SMW);
+              mx = (C::SMW == 2 ? fmaxf(mx_own, xch[(wg ^ 1) * 128 + row]) : mx_own) * eff_scale;
+              if (sc_k) ks_s[row] = k_nxt;
+              if (sc_v) vs_s[row] = v_cur * __uint_as_float((uint32_t)(259 - veb) << 23);
+              sc_warp_vmax(v_nxt);
+              v_cur = v_nxt;
+              named_bar_sync(C::NB_SMX, 128 * C::SMW);
+            } else {
+              mx = combine(mx_own, true) * eff_scale;
+            }
             const float m_new = fmaxf(m_used, mx);
             bool resc = false;
             float alpha = 1.f;
@@ -1518,17 +1624,23 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DVO, KVT, PAIR>::THREADS, 1)
               const float p0 = fast_exp2(fmaf(__uint_as_float(sr[2 * i]), eff_scale, nbase));
               const float p1 = fast_exp2(fmaf(__uint_as_float(sr[2 * i + 1]), eff_scale, nbase));
               sum4[i & 3] += p0 + p1;
-              pk[i] = C::QUANT ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+              if constexpr (SC) {
+                const float2 v2 = *reinterpret_cast<const float2*>(vs_s + col0 + 2 * i);
+                pk[i] = pack_f16x2(p0 * v2.x, p1 * v2.y);
+              } else {
+                pk[i] = C::PV16 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+              }
             }
             const float sum = (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
             // tcgen05.ld / st are warp-collective (.sync.aligned): the whole warp rescales
             // when any of its rows needs it, the other rows with a factor of 1, once the PV
             // of the previous step has finished with O
-            if (__any_sync(0xffffffffu, resc)) {
+            const float o_fac = (resc ? alpha : 1.f) * vfac;
+            if (vgrow || __any_sync(0xffffffffu, resc)) {
               mbar_wait<C::PAIR>(&pv_done[(sstep - 1) & 1], ((sstep - 1) >> 1) & 1, p.err, SITE_PRE_O_DONE);
               __syncwarp();
               tc_fence_after();
-              rescale_o(resc ? alpha : 1.f, tm_o);
+              rescale_o(o_fac, tm_o);
               if (reuse && lane == 0) {  // the second pass replays this rescale (pairs: in both CTAs)
                 rtag[jt] = tag;
                 if constexpr (C::PAIR) st_shared_cluster_u32(mapa_shared(smem_u32(&rtag[jt]), rank ^ 1), (uint32_t)tag);
@@ -1552,7 +1664,7 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DVO, KVT, PAIR>::THREADS, 1)
 #pragma unroll
               for (int k = 0; k < NCOL / 8; ++k)
                 st_global_v4_hint(prow + (size_t)(col0 / 8 + k) * (128 * 16), pk + 4 * k, pol_keep);
-              mscr[jt * 128 + row] = resc ? alpha : 1.f;
+              mscr[jt * 128 + row] = o_fac;
             }
           }
           if (reuse) {  // the P tiles of this pass are in global memory for the producer
@@ -1582,6 +1694,7 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DVO, KVT, PAIR>::THREADS, 1)
         ++n_epi;
         __syncwarp();
         tc_fence_after();
+        if constexpr (SC) v_scale = __uint_as_float((uint32_t)(veb - 5) << 23);  // 2^(veb - 132)
         const float inv = lt > 0.f ? v_scale / lt : 0.f;
         const uint32_t o_col = (reuse && pass == 1) ? tm_s : tm_o;  // this pass's O
         uint16_t* orow = p.out + ((size_t)(f.q_row0 + p_local) * p.Hq + hq) * DVO + pass * C::DVP + ocol0;

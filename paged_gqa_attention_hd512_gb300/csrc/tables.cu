@@ -1,0 +1,244 @@
+// tables.cu -- page tables on the GPU: requests that grow or shrink take pages from a free
+// list or give them back (the block table's rows follow), and a batch's block-table rows and
+// lengths become the CSR page lists, slots and positions that the other calls take.
+//
+// Pages of a length: ceil(len / page_size).  Both kernels turn the batch's page (and token)
+// counts into offsets by block-wide scans over rounds of 1024 sequences, then hand out the
+// moved or listed entries evenly over the threads, each finding its sequence by a binary
+// search among the round's ends in shared memory.  What bounds them is latency: the launch
+// and the chain length -> scan -> entry (a decode step moves a few hundred bytes, the tables
+// of 128 sequences of 32768 tokens at 16 tokens a page are 2 MB).
+#include <algorithm>
+
+#include "launch.h"
+#include "common.cuh"
+
+namespace pa {
+
+namespace {
+
+constexpr int kT = 1024;  // threads, and sequences per round
+
+// Inclusive block-wide sum of v (kT threads); s_w holds 32 words.
+__device__ __forceinline__ int block_scan(int v, int* s_w) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += t;
+  }
+  if (lane == 31) s_w[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    int w = s_w[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += t;
+    }
+    s_w[lane] = w;
+  }
+  __syncthreads();
+  v += warp > 0 ? s_w[warp - 1] : 0;
+  __syncthreads();  // s_w may be written again
+  return v;
+}
+
+__device__ __forceinline__ long long block_sum(long long v, long long* s_w) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) s_w[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0;
+#pragma unroll
+  for (int w = 0; w < 32; ++w) v += s_w[w];
+  __syncthreads();
+  return v;
+}
+
+// The first of the round's n inclusive ends that lies above x.
+__device__ __forceinline__ int find_end(const int* ends, int n, int x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (ends[mid] > x) hi = mid; else lo = mid + 1;
+  }
+  return lo;
+}
+
+struct Change {
+  int row, p_old, p_new, len_new;
+  bool bad;
+};
+
+// Sequence b's row and page counts before and after (row -1: nothing to do).
+__device__ __forceinline__ Change change_of(const ResizeParams& p, int b) {
+  Change c = {-1, 0, 0, 0, false};
+  if (b >= p.batch) return c;
+  const int row = p.row_ids ? p.row_ids[b] : b;
+  if (row < 0) return c;
+  c.bad = true;
+  if (row >= p.rows) return c;
+  const long long len = p.kv_lens[row], to = len + p.deltas[b], most = (long long)p.max_pages << p.log2_page;
+  if (len < 0 || to < 0 || len > most || to > most) return c;
+  c.bad = false;
+  c.row = row;
+  c.p_old = (int)((len + (1 << p.log2_page) - 1) >> p.log2_page);
+  c.p_new = (int)((to + (1 << p.log2_page) - 1) >> p.log2_page);
+  c.len_new = (int)to;
+  return c;
+}
+
+__global__ void __launch_bounds__(kT, 1) resize_kernel(const ResizeParams p) {
+  __shared__ int s_w[32], s_end[kT], s_row[kT], s_first[kT];
+  __shared__ long long s_l[32];
+  const int tid = threadIdx.x;
+  long long back = 0, take = 0;
+  int bad = 0;
+  for (int b = tid; b < p.batch; b += kT) {
+    const Change c = change_of(p, b);
+    bad |= c.bad;
+    back += max(c.p_old - c.p_new, 0);
+    take += max(c.p_new - c.p_old, 0);
+  }
+  bad = __syncthreads_or(bad);
+  back = block_sum(back, s_l);
+  take = block_sum(take, s_l);
+  const long long count = *p.free_count;
+  if (bad || count < 0 || count + back > p.free_size || take > count + back) {
+    if (tid == 0) record_error(p.err, SITE_RESIZE);  // nothing is changed
+    return;
+  }
+  // pages given back go behind the free list's end, in batch and table order; then pages
+  // are taken from its end
+  for (int phase = 0; phase < 2; ++phase) {
+    if (phase == 0 ? back == 0 : take == 0) continue;
+    long long done = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += kT) {
+      const Change c = change_of(p, b0 + tid);
+      const int n = phase == 0 ? max(c.p_old - c.p_new, 0) : max(c.p_new - c.p_old, 0);
+      s_end[tid] = block_scan(n, s_w);
+      s_row[tid] = c.row;
+      s_first[tid] = min(c.p_old, c.p_new) + n - s_end[tid];  // + item: the page's place in its row
+      __syncthreads();
+      const int total = s_end[kT - 1];
+      for (int i = tid; i < total; i += kT) {
+        const int k = find_end(s_end, kT, i);
+        int* entry = p.block_table + (size_t)s_row[k] * p.table_stride + s_first[k] + i;
+        if (phase == 0) p.free_pages[count + done + i] = *entry;
+        else *entry = p.free_pages[count + back - 1 - done - i];
+      }
+      done += total;
+      __syncthreads();
+    }
+  }
+  for (int b = tid; b < p.batch; b += kT) {
+    const Change c = change_of(p, b);
+    if (c.row >= 0) p.kv_lens[c.row] = c.len_new;
+  }
+  if (tid == 0) *p.free_count = (int)(count + back - take);
+}
+
+struct Listed {
+  int row, len, pages, fresh;
+  bool bad;
+};
+
+// Sequence b's row, length, pages and new tokens (all 0 for padding and for bad entries).
+__device__ __forceinline__ Listed listed_of(const BuildParams& p, int b) {
+  Listed l = {0, 0, 0, 0, false};
+  if (b >= p.batch) return l;
+  const int row = p.row_ids ? __ldg(p.row_ids + b) : b;
+  if (row < 0) return l;
+  l.bad = true;
+  if (row >= p.rows) return l;
+  const int len = __ldg(p.kv_lens + row), fresh = max(0, __ldg(p.new_counts + b));
+  if (len < 0 || len > ((long long)p.max_pages << p.log2_page) || fresh > len) return l;
+  return {row, len, (int)(((long long)len + (1 << p.log2_page) - 1) >> p.log2_page), fresh, false};
+}
+
+// Every CTA scans the whole batch (a few loads per thread) and writes its share of the
+// entries, so that one launch does without a grid-wide exchange.
+__global__ void __launch_bounds__(kT, 1) build_kernel(const BuildParams p) {
+  __shared__ int s_w[32], s_page_end[kT], s_page_first[kT], s_tok_end[kT], s_tok_first[kT], s_row[kT];
+  __shared__ long long s_l[32];
+  const int tid = threadIdx.x, ps = 1 << p.log2_page;
+  long long pages = 0, tokens = 0;
+  int bad = 0;
+  for (int b = tid; b < p.batch; b += kT) {
+    const Listed l = listed_of(p, b);
+    bad |= l.bad;
+    pages += l.pages;
+    tokens += l.fresh;
+  }
+  bad = __syncthreads_or(bad);
+  pages = block_sum(pages, s_l);
+  tokens = block_sum(tokens, s_l);
+  // more than the outputs hold: the tables of an empty batch
+  const bool none = pages > p.max_indices || tokens > p.num_tokens;
+  if ((bad || none) && blockIdx.x == 0 && tid == 0) record_error(p.err, SITE_BUILD);
+  const int first = blockIdx.x * kT + tid, step = gridDim.x * kT;
+  if (blockIdx.x == 0 && tid == 0) p.kv_indptr[0] = p.new_indptr[0] = 0;
+  int page0 = 0, tok0 = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += kT) {
+    const int b = b0 + tid;
+    Listed l = listed_of(p, b);
+    if (none) l = {0, 0, 0, 0, false};
+    const int page_end = block_scan(l.pages, s_w), tok_end = block_scan(l.fresh, s_w);
+    s_page_end[tid] = page_end;
+    s_page_first[tid] = page_end - l.pages;
+    s_tok_end[tid] = tok_end;
+    s_tok_first[tid] = l.len - tok_end;  // + token: its position
+    s_row[tid] = l.row;
+    if (blockIdx.x == 0 && b < p.batch) {
+      p.kv_indptr[b + 1] = page0 + page_end;
+      p.new_indptr[b + 1] = tok0 + tok_end;
+      p.kv_last_page_len[b] = l.len > 0 ? ((l.len - 1) & (ps - 1)) + 1 : 0;
+    }
+    __syncthreads();
+    auto page_of = [&](int k, int i) {
+      const int page = __ldg(p.block_table + (size_t)s_row[k] * p.table_stride + i);
+      if (page >= 0 && page < p.num_pages) return page;
+      record_error(p.err, SITE_BUILD);
+      return -1;
+    };
+    for (int i = first; i < s_page_end[kT - 1]; i += step) {
+      const int k = find_end(s_page_end, kT, i);
+      p.kv_indices[page0 + i] = max(0, page_of(k, i - s_page_first[k]));
+    }
+    if (p.slot_map || p.positions) {
+      for (int i = first; i < s_tok_end[kT - 1]; i += step) {
+        const int k = find_end(s_tok_end, kT, i);
+        const int pos = s_tok_first[k] + i;
+        if (p.positions) p.positions[tok0 + i] = pos;
+        if (p.slot_map) {
+          const long long page = page_of(k, pos >> p.log2_page);
+          p.slot_map[tok0 + i] = page < 0 ? -1 : (page << p.log2_page) + (pos & (ps - 1));
+        }
+      }
+    }
+    page0 += s_page_end[kT - 1];
+    tok0 += s_tok_end[kT - 1];
+    __syncthreads();
+  }
+  for (int i = tok0 + first; i < p.num_tokens; i += step) {  // rows behind the last sequence
+    if (p.slot_map) p.slot_map[i] = -1;
+    if (p.positions) p.positions[i] = -1;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_resize_tables(const ResizeParams& p, cudaStream_t s) {
+  resize_kernel<<<1, kT, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_build_tables(const BuildParams& p, int sms, cudaStream_t s) {
+  // one entry per thread, up to one CTA per SM
+  const long long most = std::max<long long>(std::max(p.max_indices, p.num_tokens), 1);
+  build_kernel<<<(int)std::min<long long>((most + kT - 1) / kT, sms), kT, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace pa
