@@ -19,29 +19,29 @@ namespace {
 
 constexpr int kT = 1024;  // threads, and sequences per round
 
-// Inclusive block-wide sum of v (kT threads); s_w holds 32 words.
-__device__ __forceinline__ int block_scan(int v, int* s_w) {
+// Inclusive block-wide sum of the two 32-bit halves of v (kT threads; the sums stay below
+// 2^32); s_w holds 33 words, the last of them the total.
+__device__ __forceinline__ unsigned long long block_scan2(unsigned long long v, unsigned long long* s_w) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int t = __shfl_up_sync(0xffffffffu, v, o);
+    const unsigned long long t = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += t;
   }
   if (lane == 31) s_w[warp] = v;
   __syncthreads();
   if (warp == 0) {
-    int w = s_w[lane];
+    unsigned long long w = s_w[lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, w, o);
+      const unsigned long long t = __shfl_up_sync(0xffffffffu, w, o);
       if (lane >= o) w += t;
     }
     s_w[lane] = w;
+    if (lane == 31) s_w[32] = w;
   }
   __syncthreads();
-  v += warp > 0 ? s_w[warp - 1] : 0;
-  __syncthreads();  // s_w may be written again
-  return v;
+  return v + (warp > 0 ? s_w[warp - 1] : 0);
 }
 
 __device__ __forceinline__ long long block_sum(long long v, long long* s_w) {
@@ -56,13 +56,12 @@ __device__ __forceinline__ long long block_sum(long long v, long long* s_w) {
   return v;
 }
 
-// The first of the round's n inclusive ends that lies above x.
-__device__ __forceinline__ int find_end(const int* ends, int n, int x) {
-  int lo = 0, hi = n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (ends[mid] > x) hi = mid; else lo = mid + 1;
-  }
+// The first of the round's kT inclusive ends that lies above x (there is one): ten steps.
+__device__ __forceinline__ int find_end(const int* ends, int x) {
+  int lo = 0;
+#pragma unroll
+  for (int step = kT / 2; step > 0; step >>= 1)
+    if (ends[lo + step - 1] <= x) lo += step;
   return lo;
 }
 
@@ -89,13 +88,25 @@ __device__ __forceinline__ Change change_of(const ResizeParams& p, int b) {
   return c;
 }
 
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// One cluster: every CTA reads lengths and count and forms the same offsets, each moves its
+// share of the pages, and the barriers order what one CTA moves against what another reads
+// (a page given back may be taken again) and the updates of lengths and count against their
+// readers.  A single CTA needed 150 us for 200 thousand pages.
 __global__ void __launch_bounds__(kT, 1) resize_kernel(const ResizeParams p) {
-  __shared__ int s_w[32], s_end[kT], s_row[kT], s_first[kT];
+  __shared__ int s_end[kT], s_row[kT], s_first[kT];
+  __shared__ unsigned long long s_w[33];
   __shared__ long long s_l[32];
-  const int tid = threadIdx.x;
-  long long back = 0, take = 0;
-  int bad = 0;
-  for (int b = tid; b < p.batch; b += kT) {
+  const int tid = threadIdx.x, part = blockIdx.x, parts = gridDim.x;
+  const long long count = *p.free_count;
+  const Change c0 = change_of(p, tid);
+  const bool one_round = p.batch <= kT;
+  long long back = max(c0.p_old - c0.p_new, 0), take = max(c0.p_new - c0.p_old, 0);
+  int bad = c0.bad;
+  for (int b = tid + kT; b < p.batch; b += kT) {
     const Change c = change_of(p, b);
     bad |= c.bad;
     back += max(c.p_old - c.p_new, 0);
@@ -104,39 +115,52 @@ __global__ void __launch_bounds__(kT, 1) resize_kernel(const ResizeParams p) {
   bad = __syncthreads_or(bad);
   back = block_sum(back, s_l);
   take = block_sum(take, s_l);
-  const long long count = *p.free_count;
   if (bad || count < 0 || count + back > p.free_size || take > count + back) {
-    if (tid == 0) record_error(p.err, SITE_RESIZE);  // nothing is changed
-    return;
+    if (part == 0 && tid == 0) record_error(p.err, SITE_RESIZE);  // nothing is changed
+    return;  // every CTA of the cluster
   }
   // pages given back go behind the free list's end, in batch and table order; then pages
   // are taken from its end
   for (int phase = 0; phase < 2; ++phase) {
     if (phase == 0 ? back == 0 : take == 0) continue;
+    if (phase == 1 && back > 0) cluster_barrier();
     long long done = 0;
     for (int b0 = 0; b0 < p.batch; b0 += kT) {
-      const Change c = change_of(p, b0 + tid);
+      const Change c = one_round ? c0 : change_of(p, b0 + tid);
       const int n = phase == 0 ? max(c.p_old - c.p_new, 0) : max(c.p_new - c.p_old, 0);
-      s_end[tid] = block_scan(n, s_w);
+      const int end = (int)block_scan2((unsigned)n, s_w);
+      s_end[tid] = end;
       s_row[tid] = c.row;
-      s_first[tid] = min(c.p_old, c.p_new) + n - s_end[tid];  // + item: the page's place in its row
+      s_first[tid] = min(c.p_old, c.p_new) + n - end;  // + item: the page's place in its row
+      const int total = (int)s_w[32];
       __syncthreads();
-      const int total = s_end[kT - 1];
-      for (int i = tid; i < total; i += kT) {
-        const int k = find_end(s_end, kT, i);
-        int* entry = p.block_table + (size_t)s_row[k] * p.table_stride + s_first[k] + i;
-        if (phase == 0) p.free_pages[count + done + i] = *entry;
-        else *entry = p.free_pages[count + back - 1 - done - i];
+      constexpr int U = 4;  // pages of a thread whose loads are in flight together
+      for (unsigned i0 = part * kT + tid; i0 < (unsigned)total; i0 += U * parts * kT) {
+        int* dst[U];
+        int page[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = (int)min(i0 + u * parts * kT, (unsigned)total - 1);
+          const int k = find_end(s_end, i);
+          int* entry = p.block_table + (size_t)s_row[k] * p.table_stride + s_first[k] + i;
+          int* listed = p.free_pages + (phase == 0 ? count + done + i : count + back - 1 - done - i);
+          dst[u] = phase == 0 ? listed : entry;
+          page[u] = __ldcg(phase == 0 ? entry : listed);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (i0 + u * parts * kT < (unsigned)total) *dst[u] = page[u];
       }
       done += total;
       __syncthreads();
     }
   }
-  for (int b = tid; b < p.batch; b += kT) {
+  cluster_barrier();  // every CTA has read lengths and count
+  for (int b = part * kT + tid; b < p.batch; b += parts * kT) {
     const Change c = change_of(p, b);
     if (c.row >= 0) p.kv_lens[c.row] = c.len_new;
   }
-  if (tid == 0) *p.free_count = (int)(count + back - take);
+  if (part == 0 && tid == 0) *p.free_count = (int)(count + back - take);
 }
 
 struct Listed {
@@ -160,12 +184,15 @@ __device__ __forceinline__ Listed listed_of(const BuildParams& p, int b) {
 // Every CTA scans the whole batch (a few loads per thread) and writes its share of the
 // entries, so that one launch does without a grid-wide exchange.
 __global__ void __launch_bounds__(kT, 1) build_kernel(const BuildParams p) {
-  __shared__ int s_w[32], s_page_end[kT], s_page_first[kT], s_tok_end[kT], s_tok_first[kT], s_row[kT];
+  __shared__ int s_page_end[kT], s_page_first[kT], s_tok_end[kT], s_tok_first[kT], s_row[kT];
+  __shared__ unsigned long long s_w[33];
   __shared__ long long s_l[32];
   const int tid = threadIdx.x, ps = 1 << p.log2_page;
-  long long pages = 0, tokens = 0;
-  int bad = 0;
-  for (int b = tid; b < p.batch; b += kT) {
+  const Listed l0 = listed_of(p, tid);
+  const bool one_round = p.batch <= kT;
+  long long pages = l0.pages, tokens = l0.fresh;
+  int bad = l0.bad;
+  for (int b = tid + kT; b < p.batch; b += kT) {
     const Listed l = listed_of(p, b);
     bad |= l.bad;
     pages += l.pages;
@@ -177,14 +204,16 @@ __global__ void __launch_bounds__(kT, 1) build_kernel(const BuildParams p) {
   // more than the outputs hold: the tables of an empty batch
   const bool none = pages > p.max_indices || tokens > p.num_tokens;
   if ((bad || none) && blockIdx.x == 0 && tid == 0) record_error(p.err, SITE_BUILD);
-  const int first = blockIdx.x * kT + tid, step = gridDim.x * kT;
+  const unsigned first = blockIdx.x * kT + tid, step = gridDim.x * kT;
   if (blockIdx.x == 0 && tid == 0) p.kv_indptr[0] = p.new_indptr[0] = 0;
   int page0 = 0, tok0 = 0;
   for (int b0 = 0; b0 < p.batch; b0 += kT) {
     const int b = b0 + tid;
-    Listed l = listed_of(p, b);
+    Listed l = one_round ? l0 : listed_of(p, b);
     if (none) l = {0, 0, 0, 0, false};
-    const int page_end = block_scan(l.pages, s_w), tok_end = block_scan(l.fresh, s_w);
+    const unsigned long long ends = block_scan2((unsigned)l.pages | (unsigned long long)(unsigned)l.fresh << 32, s_w);
+    const int page_end = (int)(unsigned)ends, tok_end = (int)(ends >> 32);
+    const int n_pages = (int)(unsigned)s_w[32], n_toks = (int)(s_w[32] >> 32);
     s_page_end[tid] = page_end;
     s_page_first[tid] = page_end - l.pages;
     s_tok_end[tid] = tok_end;
@@ -202,14 +231,14 @@ __global__ void __launch_bounds__(kT, 1) build_kernel(const BuildParams p) {
       record_error(p.err, SITE_BUILD);
       return -1;
     };
-    for (int i = first; i < s_page_end[kT - 1]; i += step) {
-      const int k = find_end(s_page_end, kT, i);
-      p.kv_indices[page0 + i] = max(0, page_of(k, i - s_page_first[k]));
+    for (unsigned i = first; i < (unsigned)n_pages; i += step) {
+      const int k = find_end(s_page_end, (int)i);
+      p.kv_indices[page0 + i] = max(0, page_of(k, (int)i - s_page_first[k]));
     }
     if (p.slot_map || p.positions) {
-      for (int i = first; i < s_tok_end[kT - 1]; i += step) {
-        const int k = find_end(s_tok_end, kT, i);
-        const int pos = s_tok_first[k] + i;
+      for (unsigned i = first; i < (unsigned)n_toks; i += step) {
+        const int k = find_end(s_tok_end, (int)i);
+        const int pos = s_tok_first[k] + (int)i;
         if (p.positions) p.positions[tok0 + i] = pos;
         if (p.slot_map) {
           const long long page = page_of(k, pos >> p.log2_page);
@@ -217,11 +246,11 @@ __global__ void __launch_bounds__(kT, 1) build_kernel(const BuildParams p) {
         }
       }
     }
-    page0 += s_page_end[kT - 1];
-    tok0 += s_tok_end[kT - 1];
+    page0 += n_pages;
+    tok0 += n_toks;
     __syncthreads();
   }
-  for (int i = tok0 + first; i < p.num_tokens; i += step) {  // rows behind the last sequence
+  for (unsigned i = tok0 + first; i < (unsigned)p.num_tokens; i += step) {  // rows behind the last sequence
     if (p.slot_map) p.slot_map[i] = -1;
     if (p.positions) p.positions[i] = -1;
   }
@@ -230,8 +259,20 @@ __global__ void __launch_bounds__(kT, 1) build_kernel(const BuildParams p) {
 }  // namespace
 
 cudaError_t launch_resize_tables(const ResizeParams& p, cudaStream_t s) {
-  resize_kernel<<<1, kT, 0, s>>>(p);
-  return cudaGetLastError();
+  // the largest portable cluster; one CTA where no more pages than its threads could move
+  const unsigned parts = (long long)p.batch * p.max_pages <= kT ? 1 : 8;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(parts);
+  cfg.blockDim = dim3(kT);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = parts;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, resize_kernel, p);
 }
 
 cudaError_t launch_build_tables(const BuildParams& p, int sms, cudaStream_t s) {
