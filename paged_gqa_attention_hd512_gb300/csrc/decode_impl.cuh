@@ -78,6 +78,76 @@ struct DecodeSmem {
 // exceeds target_chunks + batch (the workspace bound); each sequence's range is then
 // split evenly into ceil(pages / C) chunks.
 #ifdef PA_DECODE_AUX
+// Chunks for equal runs (p.shares > 0): with every sequence's visible pages laid one after the
+// other, a chunk ends at each sequence's end and at each multiple of S = ceil(total / shares)
+// pages (at least a tile of 64 tokens), so that every CTA streams the same number of pages (the last run may be short) and a
+// sequence is split only where a run ends inside it.  `total` is the visible pages.
+__device__ __forceinline__ void decode_plan_runs(const DecodeParams& p, int total, int* s_red) {
+  __shared__ int s_pages, s_chunks;
+  const int tid = threadIdx.x, ps = p.page_size;
+  const int S = max((total + p.shares - 1) / p.shares, max(1, 64 / ps));
+  // block-wide exclusive sums of v; `carry` runs over the rounds
+  auto scan = [&](int v, int* carry) {
+    const int own = v;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, v, o);
+      if ((tid & 31) >= o) v += t;
+    }
+    __syncthreads();
+    if ((tid & 31) == 31) s_red[tid >> 5] = v;
+    __syncthreads();
+    if (tid < 32) {
+      int w = (tid < (int)(blockDim.x >> 5)) ? s_red[tid] : 0;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, w, o);
+        if (tid >= o) w += t;
+      }
+      s_red[tid] = w;
+    }
+    __syncthreads();
+    const int excl = *carry + v - own + ((tid >> 5) > 0 ? s_red[(tid >> 5) - 1] : 0);
+    __syncthreads();
+    if (tid == (int)blockDim.x - 1) *carry = excl + own;
+    return excl;
+  };
+  if (tid == 0) s_pages = s_chunks = 0;
+  __syncthreads();
+  for (int base = 0; base < p.batch; base += blockDim.x) {
+    const int b = base + tid;
+    int np = 0, first = 0;
+    if (b < p.batch) {
+      np = max(0, p.kv_indptr[b + 1] - p.kv_indptr[b]);
+      if (np > 0 && p.window_left >= 0)
+        first = max(0, (np - 1) * ps + p.kv_last_page_len[b] - 1 - p.window_left) / ps;
+    }
+    const int pages = np - first;
+    const int e0 = scan(pages, &s_pages);  // the sequence's first page among all
+    const int n = pages > 0 ? (e0 + pages - 1) / S - e0 / S + 1 : 0;
+    const int c0 = scan(n, &s_chunks);
+    if (b < p.batch) {
+      p.seq_info[b] = make_int2(c0, n);
+      for (int k = 0; k < n; ++k) {
+        const int run = e0 / S + k;
+        const int lo = max(e0, run * S), hi = min(e0 + pages, (run + 1) * S);
+        DecodeChunk c;
+        c.b = b;
+        c.page_begin = first + lo - e0;
+        c.page_end = first + hi - e0;
+        c.split = k;
+        p.chunks[c0 + k] = c;
+        if (lo == run * S) p.run_first[run] = c0 + k;
+      }
+    }
+  }
+  __syncthreads();
+  for (int r = tid; r <= p.shares; r += blockDim.x)
+    if (r * (long long)S >= total) p.run_first[r] = s_chunks;  // runs without pages, and the end
+  if (tid == 0) {
+    p.hdr[0] = s_chunks;
+    p.hdr[1] = S;
+  }
+}
+
 __global__ void __launch_bounds__(1024) decode_plan_kernel(DecodeParams p) {
   __shared__ int s_red[32], s_max[32], s_min[32];
   __shared__ int s_carry;
@@ -124,6 +194,10 @@ __global__ void __launch_bounds__(1024) decode_plan_kernel(DecodeParams p) {
   }
   __syncthreads();
   const int total = s_red[0];
+  if (p.shares > 0) {
+    decode_plan_runs(p, total, s_red);
+    return;
+  }
   const bool uniform = s_max[0] > 0 && s_max[0] == s_min[0];  // every sequence the same pages
   int cp = (total + p.target_chunks - 1) / max(1, p.target_chunks);
   if (p.forced_chunk_pages > 0) {
@@ -427,7 +501,20 @@ __global__ void __launch_bounds__(DecodeCfg<KVT, DQK, DVO>::THREADS, 1)
   }
   __syncthreads();
   grid_dep_wait();  // the planner of this call is complete
-  const int n_items = p.direct ? p.batch * p.Hkv : p.hdr[0] * p.Hkv;
+  // this CTA's items: it0, it0 + step, ... below n_items
+  int n_items = p.direct ? p.batch * p.Hkv : p.hdr[0] * p.Hkv;
+  int it0 = blockIdx.x, step = gridDim.x;
+  if constexpr (C::BLK) {
+    if (!p.direct && p.shares > 0) {
+      const int run = blockIdx.x / p.Hkv;
+      step = p.Hkv;
+      it0 = n_items = 0;
+      if (run < p.shares) {
+        it0 = p.run_first[run] * p.Hkv + blockIdx.x % p.Hkv;
+        n_items = p.run_first[run + 1] * p.Hkv;
+      }
+    }
+  }
   const int ps = p.page_size;
 
   if (warp == 8) {
@@ -441,7 +528,7 @@ __global__ void __launch_bounds__(DecodeCfg<KVT, DQK, DVO>::THREADS, 1)
     }
     const int br = p.box_rows;
     uint32_t g = 0;
-    for (int it = blockIdx.x; it < n_items; it += gridDim.x) {
+    for (int it = it0; it < n_items; it += step) {
       const DecodeChunk ch = decode_item_chunk(p, it);
       const int kvh = it % p.Hkv;
       const int ip0 = p.kv_indptr[ch.b];
@@ -485,7 +572,7 @@ __global__ void __launch_bounds__(DecodeCfg<KVT, DQK, DVO>::THREADS, 1)
       float* sc0 = reinterpret_cast<float*>(smem + L::OFF_SC);
       const int lps = 31 - __clz(ps);
       uint32_t g = 0;
-      for (int it = blockIdx.x; it < n_items; it += gridDim.x) {
+      for (int it = it0; it < n_items; it += step) {
         const DecodeChunk ch = decode_item_chunk(p, it);
         const int kvh = it % p.Hkv;
         const int ip0 = p.kv_indptr[ch.b];
@@ -561,7 +648,7 @@ __global__ void __launch_bounds__(DecodeCfg<KVT, DQK, DVO>::THREADS, 1)
   constexpr int PST = L::P_STRIDE;
   uint32_t g = 0;
 
-  for (int it = blockIdx.x; it < n_items; it += gridDim.x) {
+  for (int it = it0; it < n_items; it += step) {
     const DecodeChunk ch = decode_item_chunk(p, it);
     const int kvh = it % p.Hkv;
     const int b = ch.b;

@@ -73,6 +73,11 @@ struct DecodeParams {
   int direct;
   float sm_scale;
   BlockScales bs;  // KV_INT8B / KV_FP8B
+  // KV_INT8B / KV_FP8B, when > 0: each kv head's visible pages, the sequences one after the
+  // other, are cut into `shares` equal runs, a CTA per (run, kv head); run r holds the chunks
+  // [run_first[r], run_first[r + 1])
+  int shares;
+  int* run_first;  // [shares + 1]
 };
 
 // Prefill work item: one tile of query rows (positions x heads of one kv head).
