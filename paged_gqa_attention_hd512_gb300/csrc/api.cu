@@ -157,7 +157,7 @@ EncodeTiledFn encode_fn() {
 // 3-D byte tensor [pages][rows][row_bytes] with the given page stride; boxes of
 // [1][box_rows][box_inner] bytes.
 bool make_map(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows, uint64_t pages,
-              uint64_t page_stride, uint32_t box_inner, uint32_t box_rows, bool swizzle128) {
+              uint64_t page_stride, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {row_bytes, rows, pages};
@@ -165,9 +165,8 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t row
   cuuint32_t box[3] = {box_inner, box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 
@@ -305,7 +304,7 @@ int device_sms(int* smem_optin) {
 // (the scale boxes hold whole scale rows).
 bool make_kv_maps(CUtensorMap* tk, CUtensorMap* tv, CUtensorMap* tsfk, CUtensorMap* tsfv, const void* kv_cache,
                   const uint8_t* sf, int num_pages, int Hkv, int dqk, int dvo, int ps, int kvt, int box_rows,
-                  bool swz, uint32_t box_inner = 128) {
+                  CUtensorMapSwizzle swz, uint32_t box_inner) {
   const int x2 = x2_of(kvt);
   const uint64_t k_row = (uint64_t)dqk * x2 / 2, v_row = (uint64_t)dvo * x2 / 2;
   const uint64_t rows = (uint64_t)Hkv * ps;
@@ -315,8 +314,10 @@ bool make_kv_maps(CUtensorMap* tk, CUtensorMap* tv, CUtensorMap* tsfk, CUtensorM
   if (!make_map(tv, base + rows * k_row, v_row, rows, num_pages, page_bytes, box_inner, box_rows, swz)) return false;
   if (kvt == KV_NVFP4) {
     const uint64_t sk = dqk / 16, sv = dvo / 16, sf_page = rows * (sk + sv);
-    if (!make_map(tsfk, sf, sk, rows, num_pages, sf_page, (uint32_t)sk, box_rows, false)) return false;
-    if (!make_map(tsfv, sf + rows * sk, sv, rows, num_pages, sf_page, (uint32_t)sv, box_rows, false)) return false;
+    if (!make_map(tsfk, sf, sk, rows, num_pages, sf_page, (uint32_t)sk, box_rows, CU_TENSOR_MAP_SWIZZLE_NONE))
+      return false;
+    if (!make_map(tsfv, sf + rows * sk, sv, rows, num_pages, sf_page, (uint32_t)sv, box_rows, CU_TENSOR_MAP_SWIZZLE_NONE))
+      return false;
   } else {
     *tsfk = *tk;
     *tsfv = *tv;
@@ -338,8 +339,10 @@ bool make_decode_maps(CUtensorMap* tk, CUtensorMap* tv, CUtensorMap* tsfk, CUten
   if (!make_map_rows(tv, base + rows * k_row, v_row, rows, num_pages, page_bytes, box_rows, swz)) return false;
   if (kvt == KV_NVFP4) {
     const uint64_t sk = dqk / 16, sv = dvo / 16, sf_page = rows * (sk + sv);
-    if (!make_map(tsfk, sf, sk, rows, num_pages, sf_page, (uint32_t)sk, box_rows, false)) return false;
-    if (!make_map(tsfv, sf + rows * sk, sv, rows, num_pages, sf_page, (uint32_t)sv, box_rows, false)) return false;
+    if (!make_map(tsfk, sf, sk, rows, num_pages, sf_page, (uint32_t)sk, box_rows, CU_TENSOR_MAP_SWIZZLE_NONE))
+      return false;
+    if (!make_map(tsfv, sf + rows * sk, sv, rows, num_pages, sf_page, (uint32_t)sv, box_rows, CU_TENSOR_MAP_SWIZZLE_NONE))
+      return false;
   } else {
     *tsfk = *tk;
     *tsfv = *tv;
@@ -711,11 +714,12 @@ int prefill_call(const void* q, const int32_t* qo_indptr, int total_q, const voi
   // bf16 K/V (or the bf16 copy): 128B-swizzled boxes of [page_size][64 elements], read by
   // the MMAs as they land.  FP8 / NVFP4 converted in the kernel: unswizzled boxes of the
   // packed bytes of 64 elements per key (64 / 32 B) and whole block-scale rows, staged for
-  // the converter warps.
+  // the converter warps; 64B-swizzled for codes with block scales.
   const void* kv_read = dequant ? static_cast<const void*>(ws + o_shadow) : kv_cache;
   const bool packed = run_kvt != PA_KV_BF16;
   if (!make_kv_maps(&L.tk, &L.tv, &L.tsfk, &L.tsfv, kv_read, run_kvt == KV_NVFP4 ? kv_scales->sf : nullptr, num_pages,
-                    num_kv_heads, head_dim_qk, head_dim_vo, rows_copy, run_kvt, rows_copy, !packed,
+                    num_kv_heads, head_dim_qk, head_dim_vo, rows_copy, run_kvt, rows_copy,
+                    !packed ? CU_TENSOR_MAP_SWIZZLE_128B : (scaled ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE),
                     packed ? (run_kvt == KV_NVFP4 ? 32u : 64u) : 128u))
     return PA_ERR_CUDA;
   // Q as [total_q][Hq][d_qk] bf16 bytes: boxes of [rows_per_tile][group][128 B]

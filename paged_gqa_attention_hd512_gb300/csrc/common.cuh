@@ -204,6 +204,18 @@ __device__ __forceinline__ uint32_t i8_biased_pair_f16x2(uint32_t r) {
   const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&bias));
   return *reinterpret_cast<const uint32_t*>(&d);
 }
+// Bytes A and B (0..3) of r, int8 codes, as a bf16 pair of the codes (A in the low half);
+// exact: with a code's low seven bits m and its sign bit s, the bf16 numbers 0x4300 | m and
+// 0x4300 | s << 7 are 128 + m and 128 (1 + s), and the code is m - 128 s.
+template <int A, int B>
+__device__ __forceinline__ uint32_t i8_pair_bf16x2(uint32_t r) {
+  uint32_t v;
+  asm("prmt.b32 %0, %1, 0x43434343, %2;" : "=r"(v) : "r"(r), "n"(0x4040 | A | (B << 8)));
+  const uint32_t m = v & 0xFF7FFF7Fu, s = v & 0xFF80FF80u;
+  const __nv_bfloat162 d =
+      __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&m), *reinterpret_cast<const __nv_bfloat162*>(&s));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
 // Four bytes of packed e2m1 pairs -> four f16x2 (byte k -> out[k]; low nibble -> low half).
 __device__ __forceinline__ void e2m1x8_to_f16x2x4(uint32_t src, uint32_t* out) {
   asm volatile(

@@ -1045,6 +1045,62 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DVO, KVT, PAIR, SC>::THREADS, 
       // past the end of the sequence are written as 0, whatever the slot holds.
       constexpr int FL_V = 1, FL_FIRST = 2, FL_LAST = 4, FL_END = 8;
       constexpr int RAW16 = C::CW / 16;
+      if constexpr (kv_block_scaled(KVT)) {
+        // 8-bit codes: the next half's bytes are read from the staging ring (64B-swizzled
+        // rows, so that eight lanes' 16-byte reads meet no bank twice) while this half is
+        // converted, and its stage is released as soon as they are in registers.
+        const int t = threadIdx.x - 256;
+        const uint8_t* stg = smem + C::OFF_STG;
+        uint4 raw[4];
+        int2 d;
+        auto fetch = [&](uint32_t j) {
+          const int stage = j % C::NSTG;
+          mbar_wait(&stg_full[stage], (j / C::NSTG) & 1, p.err, SITE_PRE_STG);
+          d = stg_desc[stage];
+          const bool ok = t < d.x;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            raw[q] = ok ? *reinterpret_cast<const uint4*>(stg + stage * C::STG_BYTES + t * 64 + ((q ^ ((t >> 1) & 3)) << 4))
+                        : make_uint4(0, 0, 0, 0);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&stg_empty[stage]);
+        };
+        fetch(0);
+        for (uint32_t j = 0; !(d.y & FL_END); ++j) {
+          const uint32_t w16[16] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w,
+                                    raw[2].x, raw[2].y, raw[2].z, raw[2].w, raw[3].x, raw[3].y, raw[3].z, raw[3].w};
+          const bool is_v = d.y & FL_V;
+          const uint32_t rj = j >> 1, half = j & 1;  // ring chunk and block
+          const int slot = rj % NSLOT;
+          fetch(j + 1);
+          if (half == 0) mbar_wait(&kv_empty[slot], ((rj / NSLOT) & 1) ^ 1, p.err, SITE_PRE_KV_EMPTY);
+          __syncwarp();
+          uint8_t* sp = smem + C::OFF_RING + slot * C::CHUNK + half * C::HALF + t * 128;
+#pragma unroll
+          for (int jj = 0; jj < 8; ++jj) {  // 16-byte output chunk jj = elements 8jj .. 8jj+7
+            uint32_t w[4];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const uint32_t r = w16[2 * jj + q];
+              if (KVT == KV_INT8B) {
+                w[2 * q] = is_v ? i8_biased_pair_f16x2<0, 1>(r ^ 0x80808080u) : i8_pair_bf16x2<0, 1>(r);
+                w[2 * q + 1] = is_v ? i8_biased_pair_f16x2<2, 3>(r ^ 0x80808080u) : i8_pair_bf16x2<2, 3>(r);
+              } else {
+                w[2 * q] = e4m3x2_to_f16x2(r & 0xFFFFu);
+                w[2 * q + 1] = e4m3x2_to_f16x2(r >> 16);
+                if (!is_v) {
+                  w[2 * q] = f16x2_to_bf16x2(w[2 * q]);
+                  w[2 * q + 1] = f16x2_to_bf16x2(w[2 * q + 1]);
+                }
+              }
+            }
+            *reinterpret_cast<uint4*>(sp + ((jj ^ (t & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && half == 1) mbar_arrive(&kv_full[slot]);
+        }
+      } else {
       const int t = threadIdx.x - 256;
       const uint8_t* stg = smem + C::OFF_STG;
       const uint8_t* sfb = smem + C::OFF_SF;
@@ -1077,14 +1133,7 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DVO, KVT, PAIR, SC>::THREADS, 
 #pragma unroll
         for (int jj = 0; jj < 8; ++jj) {  // 16-byte output chunk jj = elements 8jj .. 8jj+7
           uint32_t w[4];
-          if constexpr (KVT == KV_INT8B) {
-            const uint4 a = raw[jj >> 1];
-            const uint32_t w0 = ((jj & 1) ? a.z : a.x) ^ 0x80808080u, w1 = ((jj & 1) ? a.w : a.y) ^ 0x80808080u;
-            w[0] = i8_biased_pair_f16x2<0, 1>(w0);
-            w[1] = i8_biased_pair_f16x2<2, 3>(w0);
-            w[2] = i8_biased_pair_f16x2<0, 1>(w1);
-            w[3] = i8_biased_pair_f16x2<2, 3>(w1);
-          } else if constexpr (KVT != KV_NVFP4) {
+          if constexpr (KVT == KV_FP8) {
             const uint4 a = raw[jj >> 1];
             const uint32_t w0 = (jj & 1) ? a.z : a.x, w1 = (jj & 1) ? a.w : a.y;
             w[0] = e4m3x2_to_f16x2(w0 & 0xFFFFu);
@@ -1117,6 +1166,7 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DVO, KVT, PAIR, SC>::THREADS, 
         if (KVT == KV_NVFP4 && (d.y & FL_LAST)) ++nsf;
       }
       (void)FL_FIRST;
+      }
     }
   } else if ((warp == 1 || warp == 2) && rank == 0) {
     // ------------------------------------------------------- MMA issuer (1) and gate (2)
