@@ -350,8 +350,9 @@ int paged_attn_release_workspace(void);
 /* Synchronises the current device, then reports and clears the device error words that
  * kernels set when a bounded wait gives up (each stream's workspace's and, once
  * paged_attn_decode_noalloc has run on the device, the one in its fixed array):
- * *code = 0 (none) or the wait site id (a workspace's first when several are set).
- * Returns PA_OK, PA_ERR_DEVICE when a wait gave up, PA_ERR_CUDA on a CUDA error. */
+ * *code = 0 (none) or the wait site id (a workspace's first when several are set); or the
+ * code of bad data that a call met on the device: 301 an append, 401 a refused resize, 402 a
+ * table build.  Returns PA_OK, PA_ERR_DEVICE when a wait gave up, PA_ERR_CUDA on a CUDA error. */
 int paged_attn_check_device_error(int* code);
 
 /* Test hook: stores `code` in a device error word of the current device (blocking):

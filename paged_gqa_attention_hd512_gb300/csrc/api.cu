@@ -58,7 +58,10 @@ struct Workspace {
 // one grow-only workspace per (device, stream): calls on different streams may overlap on
 // the GPU, calls on one stream are ordered by it
 std::map<cudaStream_t, Workspace> g_ws[kMaxDevices];
-constexpr size_t kErrOffset = 0;      // int error word
+constexpr size_t kErrOffset = 0;      // int error word: a wait that gave up (see mbar_wait)
+// int: the caller's data (bad positions, page ids, lengths) as the block-scaled append and the
+// table calls met it.  A word of its own, since waits give up at once while the first is set.
+constexpr size_t kDataErrOffset = 4;
 constexpr size_t kFixedBytes = 256;   // error word region
 constexpr int kReuseTiles = 64;       // prefill P reuse: items of up to 64 KV tiles (8192 keys)
 constexpr uint64_t kDefaultDequantLimit = 4ull << 30;  // prefill: largest bf16 copy of FP8 / NVFP4 pages
@@ -119,7 +122,17 @@ void* workspace(size_t need, cudaStream_t stream, int* status) {
   }
   Workspace& w = g_ws[dev][stream];
   if (w.bytes >= need) return w.base;
-  if (w.base) cudaFree(w.base);
+  // the error words outlive the buffer (cudaFree waits for the device in any case)
+  int words[2] = {0, 0};
+  if (w.base) {
+    if (cudaStreamSynchronize(stream) != cudaSuccess ||
+        cudaMemcpy(words, static_cast<char*>(w.base) + kErrOffset, sizeof words, cudaMemcpyDeviceToHost) !=
+        cudaSuccess) {
+      *status = PA_ERR_CUDA;
+      return nullptr;
+    }
+    cudaFree(w.base);
+  }
   w.base = nullptr;
   w.bytes = 0;
   size_t bytes = align_up(need + need / 4, 1 << 20);
@@ -128,7 +141,8 @@ void* workspace(size_t need, cudaStream_t stream, int* status) {
     *status = PA_ERR_CUDA;
     return nullptr;
   }
-  if (cudaMemset(w.base, 0, kFixedBytes) != cudaSuccess) {
+  if (cudaMemset(w.base, 0, kFixedBytes) != cudaSuccess ||
+      cudaMemcpy(static_cast<char*>(w.base) + kErrOffset, words, sizeof words, cudaMemcpyHostToDevice) != cudaSuccess) {
     *status = PA_ERR_CUDA;
     return nullptr;
   }
@@ -187,6 +201,19 @@ bool make_map_rows(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_
                   swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+// 4-D tensor [rows][heads][d / 256][256] of 16-bit elements; boxes of box_rows rows of one head.
+bool make_row_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t heads, uint32_t d, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {256, d / 256, heads, rows};
+  cuuint64_t strides[3] = {512, (cuuint64_t)d * 2, heads * d * 2};
+  cuuint32_t box[4] = {256, d / 256, 1, box_rows};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -399,13 +426,15 @@ void* noalloc_scratch(int* status) {
   return g_noalloc_ptr[dev];
 }
 
-// Reads and clears one device error word (blocking); returns its value, or -1 on a CUDA error.
+// Reads and clears the device error words of one buffer (blocking); returns the first that is
+// set, 0, or -1 on a CUDA error.
 int take_error_word(void* base) {
-  int v = 0;
+  static_assert(kDataErrOffset == kErrOffset + sizeof(int), "the two words are adjacent");
+  int v[2] = {0, 0};
   char* e = static_cast<char*>(base) + kErrOffset;
-  if (cudaMemcpy(&v, e, sizeof v, cudaMemcpyDeviceToHost) != cudaSuccess) return -1;
-  if (v != 0 && cudaMemset(e, 0, sizeof v) != cudaSuccess) return -1;
-  return v;
+  if (cudaMemcpy(v, e, sizeof v, cudaMemcpyDeviceToHost) != cudaSuccess) return -1;
+  if ((v[0] != 0 || v[1] != 0) && cudaMemset(e, 0, sizeof v) != cudaSuccess) return -1;
+  return v[0] != 0 ? v[0] : v[1];
 }
 }  // namespace
 }  // namespace pa
@@ -948,6 +977,7 @@ int paged_attn_append_kv_block(const void* k_new, const void* v_new, const int32
   p.cache = static_cast<uint8_t*>(kv_cache);
   p.scales = scales;
   p.err = reinterpret_cast<int*>(ws + kErrOffset);
+  p.data_err = reinterpret_cast<int*>(ws + kDataErrOffset);
   p.log2_tokens = log2_of(block_tokens);
   p.per_head = page_size / block_tokens;
   p.batch = batch;
@@ -957,8 +987,22 @@ int paged_attn_append_kv_block(const void* k_new, const void* v_new, const int32
   p.d_qk = head_dim_qk;
   p.d_vo = head_dim_vo;
   p.page_size = page_size;
+  int smem_optin = 0;
+  const int sms = device_sms(&smem_optin);
+  if (sms <= 0) return PA_ERR_CUDA;
+  AppendBlockMaps tm;
+  std::memset(&tm, 0, sizeof tm);
+  if (append_block_streams(total_new, batch, block_tokens)) {
+    for (int side = 0; side < 2; ++side) {
+      const void* rows = side ? v_new : k_new;
+      const int d = side ? head_dim_vo : head_dim_qk;
+      if (!make_row_map(&tm.block[side], rows, total_new, num_kv_heads, d, block_tokens) ||
+          !make_row_map(&tm.rows[side], rows, total_new, num_kv_heads, d, append_block_box_rows()))
+        return PA_ERR_CUDA;
+    }
+  }
   prof_mark(static_cast<cudaStream_t>(stream), true);
-  const cudaError_t e = launch_append_block(kv_dtype, p, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_append_block(kv_dtype, tm, p, sms, static_cast<cudaStream_t>(stream));
   prof_mark(static_cast<cudaStream_t>(stream), false);
   if (e != cudaSuccess) return PA_ERR_CUDA;
   std::snprintf(g_variant, sizeof g_variant, "append_kv_%s", kv_names[kv_dtype]);
@@ -984,7 +1028,7 @@ int paged_attn_resize_tables(int32_t* block_table, int rows, int max_pages, int 
   p.deltas = deltas;
   p.free_pages = free_pages;
   p.free_count = free_count;
-  p.err = reinterpret_cast<int*>(ws + kErrOffset);
+  p.data_err = reinterpret_cast<int*>(ws + kDataErrOffset);
   p.batch = batch;
   p.rows = rows;
   p.max_pages = max_pages;
@@ -1029,7 +1073,7 @@ int paged_attn_build_tables(const int32_t* block_table, int rows, int max_pages,
   p.new_indptr = new_indptr;
   p.slot_map = slot_map;
   p.positions = positions;
-  p.err = reinterpret_cast<int*>(ws + kErrOffset);
+  p.data_err = reinterpret_cast<int*>(ws + kDataErrOffset);
   p.batch = batch;
   p.rows = rows;
   p.max_pages = max_pages;

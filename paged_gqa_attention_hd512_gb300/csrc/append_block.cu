@@ -14,8 +14,11 @@
 // of the inputs alone.
 //
 // Bytes: 2 read and 1 written per element, plus a scale per block.  A group of threads takes
-// one (block, kv head, side), loads its new rows once into registers (64 elements a thread),
-// finds their largest magnitude across the group and writes the codes.
+// one (block, kv head, side): it finds its new rows' largest magnitude, then writes the codes.
+// Short appends and blocks of 1 to 4 tokens load the rows into registers
+// (append_block_kernel), the others stream them through shared memory (append_stream_kernel).
+#include <algorithm>
+
 #include "launch.h"
 #include "common.cuh"
 
@@ -51,14 +54,19 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
   }
 }
 
+// Four bf16 values (two words) times r, as codes.
+template <int KVT, bool ANY>
+__device__ __forceinline__ uint32_t codes4w(uint32_t w0, uint32_t w1, float r) {
+  return codes4<KVT, ANY>(__fmul_rn(bf16_lo(w0), r), __fmul_rn(bf16_hi(w0), r), __fmul_rn(bf16_lo(w1), r),
+                          __fmul_rn(bf16_hi(w1), r));
+}
+
 // Sixteen bf16 values times r, as codes.
 template <int KVT, bool ANY>
 __device__ __forceinline__ uint4 codes16(const uint32_t* w, float r) {
   uint32_t o[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    o[k] = codes4<KVT, ANY>(__fmul_rn(bf16_lo(w[2 * k]), r), __fmul_rn(bf16_hi(w[2 * k]), r),
-                            __fmul_rn(bf16_lo(w[2 * k + 1]), r), __fmul_rn(bf16_hi(w[2 * k + 1]), r));
+  for (int k = 0; k < 4; ++k) o[k] = codes4w<KVT, ANY>(w[2 * k], w[2 * k + 1], r);
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
@@ -137,7 +145,7 @@ __global__ void __launch_bounds__(512, 2) append_block_kernel(const AppendBlockP
     }
     const int t = kv_len - n_new + (i - a0);  // position in the sequence
     if (t < 0) {  // more new rows than the sequence holds
-      if (tid == 0) record_error(p.err, SITE_APPEND_POS);
+      if (tid == 0) record_error(p.data_err, SITE_APPEND_POS);
       i += min(-t, a_end - i);
       continue;
     }
@@ -161,7 +169,7 @@ __global__ void __launch_bounds__(512, 2) append_block_kernel(const AppendBlockP
     for (int k = 0; k < kRegs; ++k)
       if (tid + k * G < pieces) load(tid + k * G, w[k]);
     if (page < 0 || page >= p.num_pages) {
-      if (tid == 0) record_error(p.err, SITE_APPEND_POS);
+      if (tid == 0) record_error(p.data_err, SITE_APPEND_POS);
       i += n;
       continue;
     }
@@ -241,25 +249,285 @@ __global__ void __launch_bounds__(512, 2) append_block_kernel(const AppendBlockP
   }
 }
 
+// ---------------------------------------------------------------------------------------
+// Long appends: persistent CTAs; producer warps stream the blocks' new rows into a ring of
+// shared-memory stages (one TMA box a block; a copy per row took the producer 84 cycles each,
+// 5400 for a block of 64), and kConsumers consumers in groups of G take a stage each, one
+// (block, kv head, side): a pass over it for the largest magnitude, one for the codes.  Several
+// groups work on different stages while the others load, which the register kernel above, two
+// CTAs an SM, does not reach: 33 thousand rows of 4 x (512 + 512) int8 91 -> 73 us (5.5 TB/s),
+// 64 thousand rows of 2 x (512 + 256) e4m3 in blocks of 16 69 -> 51 us (5.8 TB/s).  Groups that
+// keep their rows in registers between the passes, and so are fewer, took 83 us.
+constexpr int kConsumers = 768;
+constexpr int kBoxRows = 8;
+constexpr int kStreamElems = 128;  // of a consumer thread: G threads take a whole block
+// Stage n belongs to group n % groups, and the ring's length is the number of groups, so that a
+// slot always serves the same group, which is at most one phase away from its barriers (a
+// parity wait cannot tell more apart).  For the same reason a slot is always filled by the same
+// producer warp: every producer walks the blocks, and fills those of its slots.  (One producer
+// took about 1100 cycles a stage, more than a small block's bytes take.)
+constexpr int kMaxStages = kConsumers / 32;
+constexpr int kProducers = 4;  // warps
+
+struct StreamBlock {
+  int page, slot, rows, hs;  // rows 0: the end; hs: 2 * kv head + side
+};
+
+template <int KVT>
+__global__ void __launch_bounds__(kConsumers + 32 * kProducers, 1)
+    append_stream_kernel(const __grid_constant__ AppendBlockMaps tm, const AppendBlockParams p, const int G, const int stages,
+                         const int stage_bytes, const long long units) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ uint32_t s_max[2][kConsumers / 32];
+  __shared__ StreamBlock s_blk[kMaxStages];
+  __shared__ __align__(8) uint64_t s_full[kMaxStages], s_empty[kMaxStages];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int groups = kConsumers / G;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&s_full[s], 1);
+      mbar_init(&s_empty[s], G / 32);
+    }
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const int lbt = p.log2_tokens, bt = 1 << lbt, ps = p.page_size, HS = 2 * p.Hkv;
+  const size_t side_bytes = (size_t)p.Hkv * ps * p.d_qk, page_bytes = side_bytes + (size_t)p.Hkv * ps * p.d_vo;
+
+  if (warp >= kConsumers / 32) {
+    // ------------------------------------------------------------------ producers
+    const int me = warp - kConsumers / 32;
+    // unit u: the blocks whose first new row lies in rows [u / HS * bt, (u / HS + 1) * bt), for
+    // head and side u % HS; this CTA has a run of consecutive units
+    const long long u_begin = units * blockIdx.x / gridDim.x, u_end = units * (blockIdx.x + 1) / gridDim.x;
+    int s = 0;           // the next stage, and the phase of its slot
+    uint32_t phase = 0;
+    int b = -1, a0 = 0, a_end = 0, n_new = 0, ip0 = 0, kv_len = 0;
+    auto put = [&](int page, int slot, int rows, int hs, int i) -> bool {
+      const int slot_s = s;
+      const uint32_t parity = phase ^ 1;
+      if (++s == stages) {
+        s = 0;
+        phase ^= 1;
+      }
+      if (slot_s % kProducers != me) return true;
+      if (!mbar_wait(&s_empty[slot_s], parity, p.err, SITE_APPEND_RING)) return false;
+      const bool is_v = hs & 1;
+      uint64_t* full = &s_full[slot_s];
+      const uint32_t dst = smem_u32(ring) + slot_s * stage_bytes;
+      // a whole block in one box; others in boxes of kBoxRows rows, up to kBoxRows - 1 of them
+      // not the block's (0 past the last row)
+      const bool whole = rows == bt;
+      const uint32_t row_bytes = 2u * (is_v ? p.d_vo : p.d_qk), boxes = (rows + kBoxRows - 1) / kBoxRows;
+      if (lane == 0) {
+        s_blk[slot_s] = {page, slot, rows, hs};
+        if (rows > 0) mbar_arrive_expect_tx(full, boxes * kBoxRows * row_bytes);
+        else mbar_arrive(full);
+        if (whole) tma_load_4d(dst, &tm.block[is_v], 0, 0, hs >> 1, i, full);
+      }
+      if (!whole) {
+        __syncwarp();
+        if (lane < boxes)
+          tma_load_4d(dst + lane * kBoxRows * row_bytes, &tm.rows[is_v], 0, 0, hs >> 1, i + lane * kBoxRows, full);
+      }
+      return true;
+    };
+    int q0 = 0, my_page = -1;  // pages of the sequence's blocks q0 + lane
+    bool more = true;
+    for (long long c = u_begin / HS; more && c * HS < u_end; ++c) {
+      const int hs0 = (int)max(0ll, u_begin - c * HS), hs1 = (int)min((long long)HS, u_end - c * HS);
+      const int i_end = (int)min((long long)p.total_new, (c + 1) * bt);
+      for (int i = (int)(c * bt); i < i_end;) {
+        if (b < 0 || i >= a_end) {
+          // the last sequence b with append_indptr[b] <= i, 32 candidates per round
+          int lo = max(b, 0), hi = p.batch;
+          while (hi - lo > 1) {
+            const int step = (hi - lo + 31) / 32;
+            const int k = lo + step * lane;
+            const bool le = lane > 0 && k < hi && __ldg(p.append_indptr + k) <= i;
+            const unsigned m = __ballot_sync(0xffffffffu, le);
+            if (m) lo += step * (31 - __clz(m));
+            hi = min(hi, lo + step);
+          }
+          b = lo;
+          a0 = __ldg(p.append_indptr + b);
+          a_end = __ldg(p.append_indptr + b + 1);
+          n_new = a_end - a0;
+          a_end = min(a_end, p.total_new);
+          if (i < a0 || i >= a_end) {  // rows past the last sequence
+            more = false;
+            break;
+          }
+          ip0 = __ldg(p.kv_indptr + b);
+          const int np = __ldg(p.kv_indptr + b + 1) - ip0;
+          kv_len = np > 0 ? (np - 1) * ps + __ldg(p.kv_last_page_len + b) : 0;
+          q0 = -32;
+        }
+        const int t = kv_len - n_new + (i - a0);  // position in the sequence
+        if (t < 0) {  // more new rows than the sequence holds
+          if (lane == 0) record_error(p.data_err, SITE_APPEND_POS);
+          i += min(-t, a_end - i);
+          continue;
+        }
+        const int in_blk = t & (bt - 1);
+        const int rows = min(bt - in_blk, a_end - i);  // rows from i on that share its block
+        if (i == a0 || in_blk == 0) {                  // the block's first new row
+          const int q = t >> lbt;
+          if (q - q0 >= 32) {
+            q0 = q;
+            const long long first = (long long)(q + lane) << lbt;
+            my_page = first < kv_len ? __ldg(p.kv_indices + ip0 + (int)first / ps) : -1;
+          }
+          const int page = __shfl_sync(0xffffffffu, my_page, q - q0);
+          if (page < 0 || page >= p.num_pages) {
+            if (lane == 0) record_error(p.data_err, SITE_APPEND_POS);
+          } else {
+            for (int hs = hs0; hs < hs1; ++hs)
+              if (!__all_sync(0xffffffffu, put(page, t & (ps - 1), rows, hs, i))) return;
+          }
+        }
+        i += rows;
+      }
+    }
+    for (int k = 0; k < groups; ++k)  // the end, once for each group
+      if (!__all_sync(0xffffffffu, put(0, 0, 0, 0, 0))) return;
+    return;
+  }
+
+  // -------------------------------------------------------------------- consumers
+  const int group = threadIdx.x / G, tid = threadIdx.x & (G - 1);
+  uint32_t turn = 0;
+  for (uint32_t n = group;; n += groups) {
+    const int s = n % stages;
+    // (a wait that gives up leaves the error word set, and every other wait gives up at once)
+    if (!mbar_wait(&s_full[s], (n / stages) & 1, p.err, SITE_APPEND_RING)) return;
+    const StreamBlock blk = s_blk[s];
+    if (blk.rows == 0) return;
+    const bool is_v = blk.hs & 1;
+    const int h = blk.hs >> 1, d = is_v ? p.d_vo : p.d_qk;
+    const int pieces = blk.rows * (d / 8), in_blk = blk.slot & (bt - 1);
+    float* sp = p.scales + (((size_t)blk.page * 2 + (is_v ? 1 : 0)) * p.Hkv + h) * p.per_head + (blk.slot >> lbt);
+    const float s_old = in_blk > 0 ? *sp : 0.f;
+    const uint4* src = reinterpret_cast<const uint4*>(ring + (size_t)s * stage_bytes);
+    // f(u, piece u) for this thread's 8-element pieces, eight reads in flight
+    auto each = [&](auto f) {
+#pragma unroll 1
+      for (int u0 = tid; u0 < pieces; u0 += 8 * G) {
+        uint4 v[8];
+        if (u0 + 7 * G < pieces) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = src[u0 + k * G];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) f(u0 + k * G, v[k]);
+        } else {
+#pragma unroll 1
+          for (int u = u0; u < pieces; u += G) f(u, src[u]);
+        }
+      }
+    };
+    // the largest magnitude (bf16 bits; infinities and NaN are above every finite one)
+    uint32_t m2 = 0;
+    each([&](int, uint4 v) {
+      m2 = __vmaxu2(__vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                             __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)), m2);
+    });
+    auto group_max = [&](uint32_t m) -> uint32_t {
+      m = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
+      if (G == 32) return m;
+      // (the slots of two turns ago: every warp has passed the barrier in between)
+      uint32_t* slots = s_max[turn++ & 1] + group * (G / 32);
+      if (lane == 0) slots[warp & (G / 32 - 1)] = m;
+      named_bar_sync(1 + group, G);
+      for (int k = 0; k < G / 32; ++k) m = max(m, slots[k]);
+      return m;
+    };
+    uint32_t mb = group_max(m2);
+    const bool any = mb >= 0x7F80u;
+    if (any) {  // infinities or NaN: the finite values' maximum
+      m2 = 0;
+      for (int u = tid; u < pieces; u += G) {
+        const uint4 v = src[u];
+        m2 = __vmaxu2(__vmaxu2(__vmaxu2(finite_abs2(v.x), finite_abs2(v.y)),
+                               __vmaxu2(finite_abs2(v.z), finite_abs2(v.w))), m2);
+      }
+      mb = group_max(m2);
+    }
+    const float sc = fmaxf(s_old, __fmul_rn(__uint_as_float(mb << 16), KVT == KV_INT8B ? 1.f / 127.f : 1.f / 448.f));
+    const float r = sc > 0.f ? fminf(__frcp_rn(sc), 3.402823466e38f) : 0.f;
+    uint8_t* blk_rows = p.cache + (size_t)blk.page * page_bytes + (is_v ? side_bytes : 0) +
+                        ((size_t)h * ps + (blk.slot - in_blk)) * d;  // the block's first slot
+    if (in_blk > 0 && sc > s_old) {
+      const float ratio = __fmul_rn(s_old, r);
+      for (int u = tid; u < in_blk * (d / 16); u += G) {
+        uint4* q = reinterpret_cast<uint4*>(blk_rows) + u;
+        const uint4 c = *q;
+        *q = make_uint4(recode4<KVT>(c.x, ratio), recode4<KVT>(c.y, ratio), recode4<KVT>(c.z, ratio),
+                        recode4<KVT>(c.w, ratio));
+      }
+    }
+    // (with G = 32 every lane has read s_old at the maximum's reduction, else at its barrier)
+    if (tid == 0) *sp = sc;
+    uint2* dst = reinterpret_cast<uint2*>(blk_rows + (size_t)in_blk * d);
+    if (any || sc == 0.f) {
+      for (int u = tid; u < pieces; u += G) {
+        const uint4 v = src[u];
+        dst[u] = sc > 0.f ? make_uint2(codes4w<KVT, true>(v.x, v.y, r), codes4w<KVT, true>(v.z, v.w, r))
+                          : make_uint2(0, 0);
+      }
+    } else {
+      each([&](int u, uint4 v) { dst[u] = make_uint2(codes4w<KVT, false>(v.x, v.y, r), codes4w<KVT, false>(v.z, v.w, r)); });
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s_empty[s]);
+  }
+}
+
+// Few new rows a sequence (a decode step's append)
+bool append_block_steps(int total_new, int batch) { return total_new <= 4ll * batch; }
+
 }  // namespace
 
-cudaError_t launch_append_block(int kvt, const AppendBlockParams& p, cudaStream_t s) {
+bool append_block_streams(int total_new, int batch, int block_tokens) {
+  return !append_block_steps(total_new, batch) && block_tokens >= kBoxRows;
+}
+int append_block_box_rows() { return kBoxRows; }
+
+template <int KVT>
+static cudaError_t run_append(const AppendBlockMaps& tm, const AppendBlockParams& p, int sms, cudaStream_t s) {
+  const int bt = 1 << p.log2_tokens, d = std::max(p.d_qk, p.d_vo);
   // Short appends (a decode step's: few new rows a sequence): a warp per row, so that every row
   // starts at once.  Otherwise a block's worth of rows per group, among which about one block
-  // starts, and as many threads as keep the whole block in registers.
-  const bool steps = p.total_new <= 4ll * p.batch;
-  const int tokens = steps ? 1 : 1 << p.log2_tokens;
+  // starts, and as many threads as keep a whole block in registers (64 elements each).
+  const bool steps = append_block_steps(p.total_new, p.batch);
+  const int tokens = steps ? 1 : bt;
   int G = 32;
-  const int d = p.d_qk > p.d_vo ? p.d_qk : p.d_vo;
-  while (!steps && G < 512 && G * kRegs * 16 < d << p.log2_tokens) G *= 2;
-  const int threads = G > 256 ? G : 256;
   const long long units = ((long long)p.total_new + tokens - 1) / tokens * p.Hkv * 2;
+  // Streamed where a block is at least a box (8 tokens): G from 32 (8 x 256) to 256
+  // threads (64 x 512)
+  if (append_block_streams(p.total_new, p.batch, bt)) {
+    while (G * kStreamElems < d * bt) G *= 2;
+    const int stage = bt * d * 2, stages = kConsumers / G;
+    auto kern = append_stream_kernel<KVT>;
+    static std::atomic<uint64_t> smem_set;
+    const cudaError_t e = set_smem_limit_once(kern, kConsumers * kStreamElems * 2, smem_set);
+    if (e != cudaSuccess) return e;
+    kern<<<(unsigned)std::min<long long>(units, sms), kConsumers + 32 * kProducers, stages * stage, s>>>(
+        tm, p, G, stages, stage, units);
+    return cudaGetLastError();
+  }
+  while (!steps && G * 16 * kRegs < d * bt) G *= 2;
+  const int threads = G > 256 ? G : 256;
   const long long grid = (units + threads / G - 1) / (threads / G);
   if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
-  if (kvt == KV_INT8B) append_block_kernel<KV_INT8B><<<(unsigned)grid, threads, 0, s>>>(p, tokens, G);
-  else if (kvt == KV_FP8B) append_block_kernel<KV_FP8B><<<(unsigned)grid, threads, 0, s>>>(p, tokens, G);
-  else return cudaErrorInvalidValue;
+  append_block_kernel<KVT><<<(unsigned)grid, threads, 0, s>>>(p, tokens, G);
   return cudaGetLastError();
+}
+
+cudaError_t launch_append_block(int kvt, const AppendBlockMaps& tm, const AppendBlockParams& p, int sms,
+                                cudaStream_t s) {
+  if (kvt == KV_INT8B) return run_append<KV_INT8B>(tm, p, sms, s);
+  if (kvt == KV_FP8B) return run_append<KV_FP8B>(tm, p, sms, s);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace pa

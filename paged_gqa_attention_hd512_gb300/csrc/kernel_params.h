@@ -33,6 +33,7 @@ enum {
   SITE_PRE_SF = 210,
   SITE_PRE_ALIGN = 211,  // prefill: the shared memory window is not 1024-byte aligned
   SITE_APPEND_POS = 301,  // append: more new tokens than the sequence holds, or a page id out of range
+  SITE_APPEND_RING = 302,  // append into blocks: a stage of the ring
   SITE_RESIZE = 401,  // table resize: a bad row or length, no room in a row or no free page
   SITE_BUILD = 402,   // table build: a bad row, length or page id, or more entries than the outputs hold
 };
@@ -190,6 +191,7 @@ struct AppendBlockParams {
   uint8_t* cache;
   float* scales;    // [num_pages][2][Hkv][per_head]
   int* err;
+  int* data_err;
   int log2_tokens;  // tokens of a block
   int per_head;     // blocks of a page and head
   int batch, total_new, num_pages, Hkv, d_qk, d_vo, page_size;
@@ -203,7 +205,7 @@ struct ResizeParams {
   const int32_t* deltas;   // [batch]
   int32_t* free_pages;     // [free_size]
   int32_t* free_count;
-  int* err;
+  int* data_err;
   int batch, rows, max_pages, table_stride, log2_page, free_size;
 };
 
@@ -219,7 +221,7 @@ struct BuildParams {
   int32_t* new_indptr;        // [batch + 1]
   int64_t* slot_map;          // [num_tokens] or nullptr
   int32_t* positions;         // [num_tokens] or nullptr
-  int* err;
+  int* data_err;
   int batch, rows, max_pages, table_stride, log2_page, num_pages, max_indices, num_tokens;
 };
 

@@ -101,7 +101,16 @@ int prefill_pair_clusters(int dqk, int dvo);
 // New tokens' bf16 K / V -> the paged cache in its element type (quantise-on-write).
 cudaError_t launch_append_kv(int kvt, const AppendParams& p, int sms, cudaStream_t s);
 // The same into 8-bit codes with block scales (kvt KV_INT8B or KV_FP8B).
-cudaError_t launch_append_block(int kvt, const AppendBlockParams& p, cudaStream_t s);
+// tm is read only where append_block_streams says so.
+struct AppendBlockMaps {
+  // K [0] and V [1]: the new rows as [rows][Hkv][d / 256][256] 16-bit elements, boxes of one
+  // head and a whole block's or append_block_box_rows() rows
+  CUtensorMap block[2], rows[2];
+};
+cudaError_t launch_append_block(int kvt, const AppendBlockMaps& tm, const AppendBlockParams& p, int sms,
+                                cudaStream_t s);
+bool append_block_streams(int total_new, int batch, int block_tokens);
+int append_block_box_rows();
 cudaError_t launch_resize_tables(const ResizeParams& p, cudaStream_t s);
 cudaError_t launch_build_tables(const BuildParams& p, int sms, cudaStream_t s);
 

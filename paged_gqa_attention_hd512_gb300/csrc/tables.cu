@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kT, 1) resize_kernel(const ResizeParams p) {
   back = block_sum(back, s_l);
   take = block_sum(take, s_l);
   if (bad || count < 0 || count + back > p.free_size || take > count + back) {
-    if (part == 0 && tid == 0) record_error(p.err, SITE_RESIZE);  // nothing is changed
+    if (part == 0 && tid == 0) record_error(p.data_err, SITE_RESIZE);  // nothing is changed
     return;  // every CTA of the cluster
   }
   // pages given back go behind the free list's end, in batch and table order; then pages
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kT, 1) build_kernel(const BuildParams p) {
   tokens = block_sum(tokens, s_l);
   // more than the outputs hold: the tables of an empty batch
   const bool none = pages > p.max_indices || tokens > p.num_tokens;
-  if ((bad || none) && blockIdx.x == 0 && tid == 0) record_error(p.err, SITE_BUILD);
+  if ((bad || none) && blockIdx.x == 0 && tid == 0) record_error(p.data_err, SITE_BUILD);
   const unsigned first = blockIdx.x * kT + tid, step = gridDim.x * kT;
   if (blockIdx.x == 0 && tid == 0) p.kv_indptr[0] = p.new_indptr[0] = 0;
   int page0 = 0, tok0 = 0;
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kT, 1) build_kernel(const BuildParams p) {
     auto page_of = [&](int k, int i) {
       const int page = __ldg(p.block_table + (size_t)s_row[k] * p.table_stride + i);
       if (page >= 0 && page < p.num_pages) return page;
-      record_error(p.err, SITE_BUILD);
+      record_error(p.data_err, SITE_BUILD);
       return -1;
     };
     for (unsigned i = first; i < (unsigned)n_pages; i += step) {

@@ -171,6 +171,59 @@ def test_append_reports_rows_without_a_place():
     assert np.array_equal(cache.cpu().numpy()[pages], want[0][pages])
 
 
+@pytest.mark.parametrize("bt", [4, 8, 64])
+@pytest.mark.parametrize("fmt", [INT8, FP8])
+def test_append_long(fmt, bt):
+    """Several blocks per CTA of the streamed form (8 tokens a block or more), sequences that
+    begin and end inside blocks, special values, and rows behind the last sequence."""
+    c = ref.make(kv_lens=[700, 5, 1300, 64, 900], n_new=[650, 5, 1299, 64, 0], fmt=fmt, Hkv=3, d_qk=512, d_vo=256,
+                 page_size=64, bt=bt, seed=9)
+    k, v = c.k_new.float(), c.v_new.float()
+    k[100:170] = 0.0
+    k[300, 1, 5], v[301, 2, 7], v[800:900] = np.inf, np.nan, -np.inf
+    c.k_new, c.v_new = k.bfloat16(), v.bfloat16()
+    want = ref.append(c, c.cache, c.scales)
+    cache, scales = gpu(c.cache), gpu(c.scales)
+    pad = torch.full((70, 3, 512), float("nan")).bfloat16()
+    pa.paged_attn_append_kv_block(gpu(torch.cat([c.k_new, pad])), gpu(torch.cat([c.v_new, pad[..., :256]])),
+                                  gpu(c.append_indptr), cache, gpu(c.kv_indptr), gpu(c.kv_indices), gpu(c.last), scales,
+                                  page_size=64, block_tokens=bt, kv_dtype=fmt)
+    assert np.array_equal(scales.cpu().numpy(), want[1], equal_nan=True)
+    got = cache.cpu().numpy()
+    same = (got == want[0]) | ((fmt == FP8) & (got & 0x7F == 0x7F) & (want[0] & 0x7F == 0x7F))
+    assert same.all()
+
+
+@pytest.mark.parametrize("bt,ps", [(8, 8), (16, 32), (64, 64)])
+def test_append_rounds(bt, ps):
+    """Tens of blocks per CTA: the ring of the streamed form goes round many times."""
+    c = ref.make(kv_lens=[9000, 12000, 77], n_new=[8990, 12000, 70], fmt=INT8, Hkv=4, d_qk=512, d_vo=256, page_size=ps,
+                 bt=bt, seed=11)
+    want = ref.append(c, c.cache, c.scales)
+    cache, scales = gpu(c.cache), gpu(c.scales)
+    for _ in range(3):
+        pa.paged_attn_append_kv_block(gpu(c.k_new), gpu(c.v_new), gpu(c.append_indptr), cache, gpu(c.kv_indptr),
+                                      gpu(c.kv_indices), gpu(c.last), scales, page_size=ps, block_tokens=bt)
+        assert np.array_equal(scales.cpu().numpy(), want[1], equal_nan=True)
+        assert np.array_equal(cache.cpu().numpy(), want[0])
+
+
+def test_bad_data_does_not_end_the_waits_of_later_calls():
+    """The word that a refused resize or a skipped row sets is not the one that waits look at."""
+    t, n = gpu(np.zeros((1, 1), np.int32)), gpu(np.zeros(1, np.int32))
+    pa.paged_attn_resize_tables(t, None, n, gpu(np.array([5], np.int32)), n, n, page_size=16)  # no free page
+    c = ref.make(fmt=INT8, kv_lens=[5000, 300], qo_lens=[200, 300], n_new=[100, 300], Hkv=2, group=6, page_size=64,
+                 bt=32, seed=10)
+    want = ref.append(c, c.cache, c.scales)
+    cache, scales = gpu(c.cache), gpu(c.scales)
+    pa.paged_attn_append_kv_block(gpu(c.k_new), gpu(c.v_new), gpu(c.append_indptr), cache, gpu(c.kv_indptr),
+                                  gpu(c.kv_indices), gpu(c.last), scales, page_size=64, block_tokens=32)
+    assert np.array_equal(cache.cpu().numpy(), want[0])
+    out, lse = prefill(c)
+    ref.check(out, lse, ref.attend(c, c.cache, c.scales))
+    assert pa.paged_attn_check_device_error() == 401
+
+
 # ------------------------------------------------------------------------------ decode
 DECODES = [
     dict(kv_lens=[37, 64], Hkv=1, group=8, page_size=16, bt=16),
