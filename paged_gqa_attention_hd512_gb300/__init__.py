@@ -1,7 +1,9 @@
 """Paged grouped-query attention at head_dim 512 for GB300 (sm_103a): Python binding.
 
 This module only marshals arguments into the C ABI of ``libpaged_attn.so`` (declared in
-include/paged_attn.h); every step of the computation runs in the library's CUDA kernels.
+include/paged_attn.h); every step of the computation runs in the library's CUDA kernels.  The
+calls of a serving step go through a compiled module (csrc/binding.cpp), the others through
+ctypes.
 Tensors must already live on the GPU.  If the library has not been built, the calls raise
 instead of falling back to anything else.
 
@@ -13,6 +15,8 @@ instead of falling back to anything else.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 from typing import Optional, Tuple
 
@@ -20,6 +24,7 @@ import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", "libpaged_attn.so")
+BINDING_PATH = os.path.join(HERE, "_build", "_binding.so")
 
 PA_KV_BF16, PA_KV_FP8_E4M3, PA_KV_NVFP4, PA_KV_INT8_BLOCK, PA_KV_FP8_BLOCK = 0, 1, 2, 3, 4
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_ALIGNMENT = 0, -1, -2, -3
@@ -109,6 +114,23 @@ def load(path: Optional[str] = None):
     return lib
 
 
+_binding = None
+
+
+def _load_binding():
+    """The compiled binding of the serving calls (built with the library)."""
+    global _binding
+    if _binding is None:
+        load()
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(f"Python binding not built: {BINDING_PATH} is missing")
+        loader = importlib.machinery.ExtensionFileLoader("_binding", BINDING_PATH)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_binding", loader))
+        loader.exec_module(module)
+        _binding = module
+    return _binding
+
+
 def paged_attn_status_string(status: int) -> str:
     return load().paged_attn_status_string(status).decode()
 
@@ -185,18 +207,9 @@ def paged_attn_decode(q: torch.Tensor, kv_cache: torch.Tensor, kv_indptr: torch.
                       block_tokens: int = 0) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Decode: q [batch, Hq, head_dim_qk] bf16 -> out [batch, Hq, head_dim_vo] bf16, lse [batch, Hq].
     block_scales [num_pages, 2, Hkv, page_size / block_tokens] (fp32) for the block dtypes."""
-    batch, hq, dqk = q.shape
-    if num_pages is None:
-        num_pages = _num_pages(kv_cache, num_kv_heads, dqk, head_dim_vo, page_size, kv_dtype)
-    if out is None:
-        out = torch.empty(batch, hq, head_dim_vo, dtype=torch.bfloat16, device=q.device)
-    if lse is None and return_lse:
-        lse = torch.empty(batch, hq, dtype=torch.float32, device=q.device)
-    sc = _scales(kv_dtype, k_scale, v_scale, sf, block_scales, block_tokens, num_pages, num_kv_heads, page_size)
-    st = load().paged_attn_decode(_ptr(q), _ptr(kv_cache), _ptr(kv_indptr), _ptr(kv_indices),
-                                  _ptr(kv_last_page_len), batch, num_pages, hq, num_kv_heads, dqk,
-                                  head_dim_vo, page_size, float(sm_scale), window_left, kv_dtype,
-                                  ctypes.byref(sc), _ptr(out), _ptr(lse), _stream(stream))
+    st, out, lse = (_binding or _load_binding()).decode(
+        q, kv_cache, kv_indptr, kv_indices, kv_last_page_len, out, lse, return_lse, stream, num_kv_heads, head_dim_vo,
+        page_size, sm_scale, window_left, kv_dtype, k_scale, v_scale, sf, block_scales, block_tokens, num_pages)
     if st != PA_OK:
         raise PagedAttnError(st, "paged_attn_decode")
     return out, lse
@@ -240,26 +253,12 @@ def paged_attn_prefill(q: torch.Tensor, qo_indptr: torch.Tensor, kv_cache: torch
     """Prefill: q [total_q, Hq, head_dim_qk] bf16 -> out [total_q, Hq, head_dim_vo] bf16.
     custom_mask (uint8 bits) with mask_indptr (int64 byte offsets per sequence) selects
     paged_attn_prefill_custom_mask.  block_scales as for paged_attn_decode."""
-    total_q, hq, dqk = q.shape
-    batch = qo_indptr.numel() - 1
-    if num_pages is None:
-        num_pages = _num_pages(kv_cache, num_kv_heads, dqk, head_dim_vo, page_size, kv_dtype)
-    if out is None:
-        out = torch.empty(total_q, hq, head_dim_vo, dtype=torch.bfloat16, device=q.device)
-    if lse is None and return_lse:
-        lse = torch.empty(total_q, hq, dtype=torch.float32, device=q.device)
-    sc = _scales(kv_dtype, k_scale, v_scale, sf, block_scales, block_tokens, num_pages, num_kv_heads, page_size)
-    args = (_ptr(q), _ptr(qo_indptr), total_q, _ptr(kv_cache), _ptr(kv_indptr), _ptr(kv_indices),
-            _ptr(kv_last_page_len), batch, num_pages, hq, num_kv_heads, dqk, head_dim_vo, page_size,
-            float(sm_scale), window_left, int(bool(causal)), kv_dtype, ctypes.byref(sc), _ptr(out), _ptr(lse))
-    if custom_mask is not None:
-        st = load().paged_attn_prefill_custom_mask(*args, _ptr(custom_mask), _ptr(mask_indptr), _stream(stream))
-        what = "paged_attn_prefill_custom_mask"
-    else:
-        st = load().paged_attn_prefill(*args, _stream(stream))
-        what = "paged_attn_prefill"
+    st, out, lse = (_binding or _load_binding()).prefill(
+        q, qo_indptr, kv_cache, kv_indptr, kv_indices, kv_last_page_len, bool(causal), custom_mask, mask_indptr, out,
+        lse, return_lse, stream, num_kv_heads, head_dim_vo, page_size, sm_scale, window_left, kv_dtype, k_scale,
+        v_scale, sf, block_scales, block_tokens, num_pages)
     if st != PA_OK:
-        raise PagedAttnError(st, what)
+        raise PagedAttnError(st, "paged_attn_prefill" if custom_mask is None else "paged_attn_prefill_custom_mask")
     return out, lse
 
 
@@ -292,30 +291,11 @@ def paged_attn_append_kv_block(k_new: torch.Tensor, v_new: torch.Tensor, append_
     """Write k_new [total_new, Hkv, head_dim_qk] / v_new [total_new, Hkv, head_dim_vo] (bf16) as
     8-bit codes of the last tokens of each sequence, and the scales of the blocks they fall
     into: block_scales [num_pages, 2, Hkv, page_size / block_tokens] (fp32)."""
-    total_new, hkv, dqk = k_new.shape
-    dvo = v_new.shape[2]
-    if tuple(v_new.shape[:2]) != (total_new, hkv) or k_new.dtype != torch.bfloat16 or v_new.dtype != torch.bfloat16:
-        raise ValueError("k_new and v_new must be bf16 with the same rows and kv heads")
-    batch = append_indptr.numel() - 1
-    if num_pages is None:
-        num_pages = _num_pages(kv_cache, hkv, dqk, dvo, page_size, kv_dtype)
-    st = load().paged_attn_append_kv_block(
-        _ptr(k_new), _ptr(v_new), _ptr(append_indptr), total_new, _ptr(kv_cache), _ptr(kv_indptr), _ptr(kv_indices), _ptr(kv_last_page_len),
-        batch, num_pages, hkv, dqk, dvo, page_size, kv_dtype,
-        _block_scales(block_scales, block_tokens, num_pages, hkv, page_size), block_tokens, _stream(stream))
+    st = (_binding or _load_binding()).append_kv_block(
+        k_new, v_new, append_indptr, kv_cache, kv_indptr, kv_indices, kv_last_page_len, block_scales, page_size,
+        block_tokens, kv_dtype, num_pages, stream)
     if st != PA_OK:
         raise PagedAttnError(st, "paged_attn_append_kv_block")
-
-
-def _table(block_table: torch.Tensor):
-    """(pointer, rows, max_pages, row stride) of an int32 block table whose rows are contiguous."""
-    if not block_table.is_cuda:
-        raise ValueError("tensor arguments must be CUDA tensors")
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or \
-            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError("block_table must be int32 [rows, max_pages] with contiguous rows")
-    rows, width = block_table.shape
-    return block_table.data_ptr(), rows, width, max(block_table.stride(0), width)
 
 
 def paged_attn_resize_tables(block_table: torch.Tensor, row_ids: Optional[torch.Tensor], kv_lens: torch.Tensor,
@@ -324,13 +304,8 @@ def paged_attn_resize_tables(block_table: torch.Tensor, row_ids: Optional[torch.
     """Change the length of sequence b (row row_ids[b] of block_table [rows, max_pages], or row b)
     by deltas[b] tokens, moving pages between its row and the free list (free_pages, the first
     free_count[0] entries free); kv_lens [rows] and free_count [1] are updated.  All int32."""
-    ptr, rows, width, stride = _table(block_table)
-    batch, i32 = deltas.numel(), torch.int32
-    st = load().paged_attn_resize_tables(
-        ptr, rows, width, stride, None if row_ids is None else _typed(row_ids, i32, batch, "row_ids"),
-        _typed(kv_lens, i32, rows, "kv_lens"), _typed(deltas, i32, batch, "deltas"), batch, page_size,
-        _typed(free_pages, i32, 0, "free_pages"), free_pages.numel(), _typed(free_count, i32, 1, "free_count"),
-        _stream(stream))
+    st = (_binding or _load_binding()).resize_tables(block_table, row_ids, kv_lens, deltas, free_pages, free_count,
+                                                     page_size, stream)
     if st != PA_OK:
         raise PagedAttnError(st, "paged_attn_resize_tables")
 
@@ -343,21 +318,8 @@ def paged_attn_build_tables(block_table: torch.Tensor, row_ids: Optional[torch.T
     (kv_indptr [batch + 1], kv_indices [max_indices], kv_last_page_len [batch], new_indptr
     [batch + 1], slot_map int64 [num_tokens], positions [num_tokens]), int32 but for slot_map.
     max_indices and num_tokens are capacities; ``out`` gives the six tensors to write."""
-    ptr, rows, width, stride = _table(block_table)
-    batch, i32 = new_counts.numel(), torch.int32
-    if out is None:
-        dev = block_table.device
-        sizes = (batch + 1, max_indices, batch, batch + 1)
-        out = tuple(torch.empty(n, dtype=i32, device=dev) for n in sizes) + (
-            torch.empty(num_tokens, dtype=torch.int64, device=dev), torch.empty(num_tokens, dtype=i32, device=dev))
-    indptr, indices, last, new_indptr, slots, positions = out
-    st = load().paged_attn_build_tables(
-        ptr, rows, width, stride, None if row_ids is None else _typed(row_ids, i32, batch, "row_ids"),
-        _typed(kv_lens, i32, rows, "kv_lens"), _typed(new_counts, i32, batch, "new_counts"), batch, page_size,
-        num_pages, _typed(indptr, i32, batch + 1, "kv_indptr"), _typed(indices, i32, max_indices, "kv_indices"),
-        max_indices, _typed(last, i32, batch, "kv_last_page_len"), _typed(new_indptr, i32, batch + 1, "new_indptr"),
-        _typed(slots, torch.int64, num_tokens, "slot_map"), _typed(positions, i32, num_tokens, "positions"),
-        num_tokens, _stream(stream))
+    st, out = (_binding or _load_binding()).build_tables(block_table, row_ids, kv_lens, new_counts, page_size,
+                                                         num_pages, max_indices, num_tokens, out, stream)
     if st != PA_OK:
         raise PagedAttnError(st, "paged_attn_build_tables")
     return out

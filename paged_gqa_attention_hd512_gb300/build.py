@@ -1,4 +1,5 @@
-"""Compile the CUDA library (libpaged_attn.so) in-tree for sm_103a.
+"""Compile the CUDA library (libpaged_attn.so) in-tree for sm_103a, and the Python binding's
+module (_binding.so: csrc/binding.cpp, compiled with g++ against the installed torch).
 
 Every translation unit under csrc/ is compiled in parallel with nvcc, then linked into
 _build/libpaged_attn.so (CUDA runtime linked statically; the CUDA driver API's tensor-map encoder
@@ -17,6 +18,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libpaged_attn.so")
+BINDING = os.path.join(BUILD, "_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I" + os.path.join(ROOT, "include"), "-I" + CSRC]
@@ -32,9 +34,9 @@ def sources():
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     for f in os.listdir(CSRC):
         if os.path.getmtime(os.path.join(CSRC, f)) > t:
             return True
@@ -58,12 +60,44 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         return obj
 
     with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, srcs))
     tmp = LIB + ".tmp"
     cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + objs
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    link_binding(binding.result())
     return LIB
+
+
+def compile_binding() -> str:
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc())) if os.path.isabs(nvcc()) else "/usr/local/cuda"
+    obj = os.path.join(BUILD, "binding.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I" + os.path.join(ROOT, "include"), "-isystem" + os.path.join(root, "include"),
+           "-isystem" + os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem" + os.path.join(cuda, "include"), "-I" + sysconfig.get_paths()["include"],
+           "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
+        raise RuntimeError("g++ failed on binding.cpp")
+    return obj
+
+
+def link_binding(obj: str) -> None:
+    import torch
+
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"), "-L" + BUILD,
+           "-lpaged_attn", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BINDING)
 
 
 if __name__ == "__main__":
