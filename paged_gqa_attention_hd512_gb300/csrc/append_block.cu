@@ -97,6 +97,8 @@ __global__ void __launch_bounds__(512, 2) append_block_kernel(const AppendBlockP
   __shared__ uint32_t s_max[2][32];  // per warp, in turn: the largest magnitude
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int group = threadIdx.x / G, tid = threadIdx.x & (G - 1);
+  grid_dep_launch();  // the next call's kernel may start its set-up (it waits for this grid)
+  grid_dep_wait();
   const long long unit = (long long)blockIdx.x * (blockDim.x / G) + group;
   const bool is_v = unit & 1;
   const int h = (int)((unit >> 1) % p.Hkv);
@@ -291,6 +293,7 @@ __global__ void __launch_bounds__(kConsumers + 32 * kProducers, 1)
     fence_mbar_init();
   }
   __syncthreads();
+  grid_dep_wait();
   const int lbt = p.log2_tokens, bt = 1 << lbt, ps = p.page_size, HS = 2 * p.Hkv;
   const size_t side_bytes = (size_t)p.Hkv * ps * p.d_qk, page_bytes = side_bytes + (size_t)p.Hkv * ps * p.d_vo;
 
@@ -511,16 +514,14 @@ static cudaError_t run_append(const AppendBlockMaps& tm, const AppendBlockParams
     static std::atomic<uint64_t> smem_set;
     const cudaError_t e = set_smem_limit_once(kern, kConsumers * kStreamElems * 2, smem_set);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)std::min<long long>(units, sms), kConsumers + 32 * kProducers, stages * stage, s>>>(
-        tm, p, G, stages, stage, units);
-    return cudaGetLastError();
+    return launch_pdl(kern, dim3((unsigned)std::min<long long>(units, sms)), dim3(kConsumers + 32 * kProducers),
+                      stages * stage, s, 1, tm, p, G, stages, stage, units);
   }
   while (!steps && G * 16 * kRegs < d * bt) G *= 2;
   const int threads = G > 256 ? G : 256;
   const long long grid = (units + threads / G - 1) / (threads / G);
   if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
-  append_block_kernel<KVT><<<(unsigned)grid, threads, 0, s>>>(p, tokens, G);
-  return cudaGetLastError();
+  return launch_pdl(append_block_kernel<KVT>, dim3((unsigned)grid), dim3(threads), 0, s, 1, p, tokens, G);
 }
 
 cudaError_t launch_append_block(int kvt, const AppendBlockMaps& tm, const AppendBlockParams& p, int sms,

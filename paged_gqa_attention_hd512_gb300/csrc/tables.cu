@@ -7,7 +7,9 @@
 // moved or listed entries evenly over the threads, each finding its sequence by a binary
 // search among the round's ends in shared memory.  What bounds them is latency: the launch
 // and the chain length -> scan -> entry (a decode step moves a few hundred bytes, the tables
-// of 128 sequences of 32768 tokens at 16 tokens a page are 2 MB).
+// of 128 sequences of 32768 tokens at 16 tokens a page are 2 MB).  Both are launched as
+// programmatic dependents and let their own dependents launch at once, so that the kernels of a
+// step (resize, build, append, decode) overlap their launches.
 #include <algorithm>
 
 #include "launch.h"
@@ -101,6 +103,8 @@ __global__ void __launch_bounds__(kT, 1) resize_kernel(const ResizeParams p) {
   __shared__ unsigned long long s_w[33];
   __shared__ long long s_l[32];
   const int tid = threadIdx.x, part = blockIdx.x, parts = gridDim.x;
+  grid_dep_launch();  // the next call's kernel may start its set-up (it waits for this grid)
+  grid_dep_wait();
   const long long count = *p.free_count;
   const Change c0 = change_of(p, tid);
   const bool one_round = p.batch <= kT;
@@ -188,6 +192,8 @@ __global__ void __launch_bounds__(kT, 1) build_kernel(const BuildParams p) {
   __shared__ unsigned long long s_w[33];
   __shared__ long long s_l[32];
   const int tid = threadIdx.x, ps = 1 << p.log2_page;
+  grid_dep_launch();
+  grid_dep_wait();
   const Listed l0 = listed_of(p, tid);
   const bool one_round = p.batch <= kT;
   long long pages = l0.pages, tokens = l0.fresh;
@@ -261,25 +267,13 @@ __global__ void __launch_bounds__(kT, 1) build_kernel(const BuildParams p) {
 cudaError_t launch_resize_tables(const ResizeParams& p, cudaStream_t s) {
   // the largest portable cluster; one CTA where no more pages than its threads could move
   const unsigned parts = (long long)p.batch * p.max_pages <= kT ? 1 : 8;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(parts);
-  cfg.blockDim = dim3(kT);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = parts;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, resize_kernel, p);
+  return launch_pdl(resize_kernel, dim3(parts), dim3(kT), 0, s, parts, p);
 }
 
 cudaError_t launch_build_tables(const BuildParams& p, int sms, cudaStream_t s) {
   // one entry per thread, up to one CTA per SM
   const long long most = std::max<long long>(std::max(p.max_indices, p.num_tokens), 1);
-  build_kernel<<<(int)std::min<long long>((most + kT - 1) / kT, sms), kT, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_pdl(build_kernel, dim3((unsigned)std::min<long long>((most + kT - 1) / kT, sms)), dim3(kT), 0, s, 1, p);
 }
 
 }  // namespace pa
