@@ -21,29 +21,31 @@ namespace {
 
 constexpr int kT = 1024;  // threads, and sequences per round
 
-// Inclusive block-wide sum of the two 32-bit halves of v (kT threads; the sums stay below
-// 2^32); s_w holds 33 words, the last of them the total.
-__device__ __forceinline__ unsigned long long block_scan2(unsigned long long v, unsigned long long* s_w) {
+// Inclusive block-wide sums of a and of b (kT threads); w holds the totals in w[.][32].
+struct ScanWords {
+  long long w[2][33];
+};
+__device__ __forceinline__ void block_scan(long long& a, long long& b, ScanWords& s) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long t = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += t;
+    const long long ta = __shfl_up_sync(0xffffffffu, a, o), tb = __shfl_up_sync(0xffffffffu, b, o);
+    if (lane >= o) a += ta, b += tb;
   }
-  if (lane == 31) s_w[warp] = v;
+  if (lane == 31) s.w[0][warp] = a, s.w[1][warp] = b;
   __syncthreads();
-  if (warp == 0) {
-    unsigned long long w = s_w[lane];
+  if (warp < 2) {  // a warp for each of the sums
+    long long v = s.w[warp][lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long t = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += t;
+      const long long t = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += t;
     }
-    s_w[lane] = w;
-    if (lane == 31) s_w[32] = w;
+    s.w[warp][lane] = v;
+    if (lane == 31) s.w[warp][32] = v;
   }
   __syncthreads();
-  return v + (warp > 0 ? s_w[warp - 1] : 0);
+  if (warp > 0) a += s.w[0][warp - 1], b += s.w[1][warp - 1];
 }
 
 __device__ __forceinline__ long long block_sum(long long v, long long* s_w) {
@@ -100,7 +102,7 @@ __device__ __forceinline__ void cluster_barrier() {
 // readers.  A single CTA needed 150 us for 200 thousand pages.
 __global__ void __launch_bounds__(kT, 1) resize_kernel(const ResizeParams p) {
   __shared__ int s_end[kT], s_row[kT], s_first[kT];
-  __shared__ unsigned long long s_w[33];
+  __shared__ ScanWords s_w;
   __shared__ long long s_l[32];
   const int tid = threadIdx.x, part = blockIdx.x, parts = gridDim.x;
   grid_dep_launch();  // the next call's kernel may start its set-up (it waits for this grid)
@@ -117,8 +119,16 @@ __global__ void __launch_bounds__(kT, 1) resize_kernel(const ResizeParams p) {
     take += max(c.p_new - c.p_old, 0);
   }
   bad = __syncthreads_or(bad);
-  back = block_sum(back, s_l);
-  take = block_sum(take, s_l);
+  // ends of this thread's sequence among the pages given back and among those taken
+  long long end_back = back, end_take = take;
+  if (one_round) {
+    block_scan(end_back, end_take, s_w);
+    back = s_w.w[0][32];
+    take = s_w.w[1][32];
+  } else {
+    back = block_sum(back, s_l);
+    take = block_sum(take, s_l);
+  }
   if (bad || count < 0 || count + back > p.free_size || take > count + back) {
     if (part == 0 && tid == 0) record_error(p.data_err, SITE_RESIZE);  // nothing is changed
     return;  // every CTA of the cluster
@@ -132,11 +142,15 @@ __global__ void __launch_bounds__(kT, 1) resize_kernel(const ResizeParams p) {
     for (int b0 = 0; b0 < p.batch; b0 += kT) {
       const Change c = one_round ? c0 : change_of(p, b0 + tid);
       const int n = phase == 0 ? max(c.p_old - c.p_new, 0) : max(c.p_new - c.p_old, 0);
-      const int end = (int)block_scan2((unsigned)n, s_w);
+      if (!one_round) {
+        end_back = end_take = n;
+        block_scan(end_back, end_take, s_w);
+      }
+      const int end = (int)(phase == 0 ? end_back : end_take);
       s_end[tid] = end;
       s_row[tid] = c.row;
       s_first[tid] = min(c.p_old, c.p_new) + n - end;  // + item: the page's place in its row
-      const int total = (int)s_w[32];
+      const int total = (int)s_w.w[phase][32];
       __syncthreads();
       constexpr int U = 4;  // pages of a thread whose loads are in flight together
       for (unsigned i0 = part * kT + tid; i0 < (unsigned)total; i0 += U * parts * kT) {
@@ -160,9 +174,12 @@ __global__ void __launch_bounds__(kT, 1) resize_kernel(const ResizeParams p) {
     }
   }
   cluster_barrier();  // every CTA has read lengths and count
-  for (int b = part * kT + tid; b < p.batch; b += parts * kT) {
-    const Change c = change_of(p, b);
-    if (c.row >= 0) p.kv_lens[c.row] = c.len_new;
+  if (part == 0) {
+    if (c0.row >= 0) p.kv_lens[c0.row] = c0.len_new;
+    for (int b = tid + kT; b < p.batch; b += kT) {
+      const Change c = change_of(p, b);
+      if (c.row >= 0) p.kv_lens[c.row] = c.len_new;
+    }
   }
   if (part == 0 && tid == 0) *p.free_count = (int)(count + back - take);
 }
@@ -189,7 +206,7 @@ __device__ __forceinline__ Listed listed_of(const BuildParams& p, int b) {
 // entries, so that one launch does without a grid-wide exchange.
 __global__ void __launch_bounds__(kT, 1) build_kernel(const BuildParams p) {
   __shared__ int s_page_end[kT], s_page_first[kT], s_tok_end[kT], s_tok_first[kT], s_row[kT];
-  __shared__ unsigned long long s_w[33];
+  __shared__ ScanWords s_w;
   __shared__ long long s_l[32];
   const int tid = threadIdx.x, ps = 1 << p.log2_page;
   grid_dep_launch();
@@ -205,8 +222,15 @@ __global__ void __launch_bounds__(kT, 1) build_kernel(const BuildParams p) {
     tokens += l.fresh;
   }
   bad = __syncthreads_or(bad);
-  pages = block_sum(pages, s_l);
-  tokens = block_sum(tokens, s_l);
+  long long end_pages = pages, end_tokens = tokens;  // of this thread's sequence
+  if (one_round) {
+    block_scan(end_pages, end_tokens, s_w);
+    pages = s_w.w[0][32];
+    tokens = s_w.w[1][32];
+  } else {
+    pages = block_sum(pages, s_l);
+    tokens = block_sum(tokens, s_l);
+  }
   // more than the outputs hold: the tables of an empty batch
   const bool none = pages > p.max_indices || tokens > p.num_tokens;
   if ((bad || none) && blockIdx.x == 0 && tid == 0) record_error(p.data_err, SITE_BUILD);
@@ -217,9 +241,13 @@ __global__ void __launch_bounds__(kT, 1) build_kernel(const BuildParams p) {
     const int b = b0 + tid;
     Listed l = one_round ? l0 : listed_of(p, b);
     if (none) l = {0, 0, 0, 0, false};
-    const unsigned long long ends = block_scan2((unsigned)l.pages | (unsigned long long)(unsigned)l.fresh << 32, s_w);
-    const int page_end = (int)(unsigned)ends, tok_end = (int)(ends >> 32);
-    const int n_pages = (int)(unsigned)s_w[32], n_toks = (int)(s_w[32] >> 32);
+    if (!one_round) {
+      end_pages = l.pages;
+      end_tokens = l.fresh;
+      block_scan(end_pages, end_tokens, s_w);
+    }
+    const int page_end = none ? 0 : (int)end_pages, tok_end = none ? 0 : (int)end_tokens;
+    const int n_pages = none ? 0 : (int)s_w.w[0][32], n_toks = none ? 0 : (int)s_w.w[1][32];
     s_page_end[tid] = page_end;
     s_page_first[tid] = page_end - l.pages;
     s_tok_end[tid] = tok_end;
