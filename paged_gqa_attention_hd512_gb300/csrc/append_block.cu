@@ -87,13 +87,14 @@ __device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio) {
                            __fmul_rn(x[3], ratio));
 }
 
+constexpr int kStepWarps = 8;  // warps per CTA of append_step_kernel
 constexpr int kRegs = 4;  // 16-element pieces of a block's new rows that a thread keeps
 
-// A group of G threads (a power of two, at least a warp) takes the blocks whose first new row
-// lies among `tokens` consecutive new rows, for one kv head and side; blockDim.x / G groups
-// per CTA.  New rows beyond what the group's registers hold are read a second time.
+// Long appends in blocks of fewer tokens than a TMA box.  A group of G threads (a power of two,
+// at least a warp) takes the blocks whose first new row lies among a block's worth of
+// consecutive new rows, for one kv head and side; blockDim.x / G groups per CTA.
 template <int KVT>
-__global__ void __launch_bounds__(512, 2) append_block_kernel(const AppendBlockParams p, const int tokens, const int G) {
+__global__ void __launch_bounds__(512, 2) append_block_kernel(const AppendBlockParams p, const int G) {
   __shared__ uint32_t s_max[2][32];  // per warp, in turn: the largest magnitude
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int group = threadIdx.x / G, tid = threadIdx.x & (G - 1);
@@ -102,10 +103,10 @@ __global__ void __launch_bounds__(512, 2) append_block_kernel(const AppendBlockP
   const long long unit = (long long)blockIdx.x * (blockDim.x / G) + group;
   const bool is_v = unit & 1;
   const int h = (int)((unit >> 1) % p.Hkv);
-  const long long i_first = (unit >> 1) / p.Hkv * tokens;
-  if (i_first >= p.total_new) return;  // the whole group
-  const int i_end = (int)min((long long)p.total_new, i_first + tokens);
   const int lbt = p.log2_tokens, bt = 1 << lbt, ps = p.page_size;
+  const long long i_first = (unit >> 1) / p.Hkv << lbt;
+  if (i_first >= p.total_new) return;  // the whole group
+  const int i_end = (int)min((long long)p.total_new, i_first + bt);
   const int d = is_v ? p.d_vo : p.d_qk;
   const int lrow = d == 512 ? 5 : 4;  // log2 of a row's 16-element pieces
   const size_t row_elems = (size_t)p.Hkv * d;
@@ -122,14 +123,6 @@ __global__ void __launch_bounds__(512, 2) append_block_kernel(const AppendBlockP
     kv_len = k1 > k0 ? (k1 - k0 - 1) * ps + last : 0;
   };
   for (int i = (int)i_first; i < i_end;) {
-    if (b < 0) {
-      // a batch of single tokens has row i in sequence i: look there first, with every load
-      // that the sequence needs in flight at once
-      const int g = min(i, p.batch - 1);
-      const int lo = __ldg(p.append_indptr + g), hi = __ldg(p.append_indptr + g + 1);
-      const int k0 = __ldg(p.kv_indptr + g), k1 = __ldg(p.kv_indptr + g + 1), last = __ldg(p.kv_last_page_len + g);
-      if (lo <= i && i < hi) enter(g, lo, hi, k0, k1, last);
-    }
     if (b < 0 || i >= a_end) {
       // the last sequence b with append_indptr[b] <= i, 32 candidates per round
       int lo = max(b, 0), hi = p.batch;
@@ -248,6 +241,115 @@ __global__ void __launch_bounds__(512, 2) append_block_kernel(const AppendBlockP
       }
     }
     i += n;
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// Short appends (a decode step's, few new rows a sequence): a warp per (new row, kv head), K and
+// V together.  What takes time is the chain of dependent loads, so the row's values are loaded
+// at once, beside the guess that row i belongs to sequence i; then the page id, then the old
+// scales.  A warp whose row is not its block's first new one leaves; one whose block has more
+// new rows reads those too.
+template <int KVT>
+__global__ void __launch_bounds__(32 * kStepWarps, 4) append_step_kernel(const AppendBlockParams p) {
+  const int lane = threadIdx.x & 31;
+  const long long unit = (long long)blockIdx.x * kStepWarps + (threadIdx.x >> 5);
+  grid_dep_launch();  // the next call's kernel may start its set-up (it waits for this grid)
+  grid_dep_wait();
+  const int h = (int)(unit % p.Hkv);
+  if (unit / p.Hkv >= p.total_new) return;
+  const int i = (int)(unit / p.Hkv);
+  const int lbt = p.log2_tokens, bt = 1 << lbt, ps = p.page_size;
+  // 8-element pieces lane and lane + 32 (512 elements) of row r of a side
+  auto load_row = [&](int side, int r, uint4* w) {
+    const int d = side ? p.d_vo : p.d_qk;
+    const uint4* src = reinterpret_cast<const uint4*>((side ? p.v_new : p.k_new) + ((size_t)r * p.Hkv + h) * d);
+    w[0] = __ldg(src + lane);
+    w[1] = d == 512 ? __ldg(src + lane + 32) : make_uint4(0, 0, 0, 0);
+  };
+  uint4 w[2][2];
+  load_row(0, i, w[0]);
+  load_row(1, i, w[1]);
+  int b = min(i, p.batch - 1);
+  int a0 = __ldg(p.append_indptr + b), a_end = __ldg(p.append_indptr + b + 1);
+  int ip0 = __ldg(p.kv_indptr + b), ip1 = __ldg(p.kv_indptr + b + 1), last = __ldg(p.kv_last_page_len + b);
+  if (i < a0 || i >= a_end) {
+    // the last sequence b with append_indptr[b] <= i, 32 candidates per round
+    int lo = 0, hi = p.batch;
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32;
+      const int c = lo + step * lane;
+      const bool le = lane > 0 && c < hi && __ldg(p.append_indptr + c) <= i;
+      const unsigned m = __ballot_sync(0xffffffffu, le);
+      if (m) lo += step * (31 - __clz(m));
+      hi = min(hi, lo + step);
+    }
+    b = lo;
+    a0 = __ldg(p.append_indptr + b);
+    a_end = __ldg(p.append_indptr + b + 1);
+    ip0 = __ldg(p.kv_indptr + b);
+    ip1 = __ldg(p.kv_indptr + b + 1);
+    last = __ldg(p.kv_last_page_len + b);
+    if (i < a0 || i >= a_end) return;  // rows past the last sequence
+  }
+  const int kv_len = ip1 > ip0 ? (ip1 - ip0 - 1) * ps + last : 0;
+  const int t = kv_len - (a_end - a0) + (i - a0);  // position in the sequence
+  if (t < 0) {                                     // more new rows than the sequence holds
+    if (lane == 0) record_error(p.data_err, SITE_APPEND_POS);
+    return;
+  }
+  const int in_blk = t & (bt - 1), slot = t & (ps - 1);
+  if (i > a0 && in_blk > 0) return;  // not the block's first new row
+  const int n = min(bt - in_blk, min(a_end, p.total_new) - i);
+  const int page = __ldg(p.kv_indices + ip0 + t / ps);
+  if (page < 0 || page >= p.num_pages) {
+    if (lane == 0) record_error(p.data_err, SITE_APPEND_POS);
+    return;
+  }
+  float* sp = p.scales + ((size_t)page * 2 * p.Hkv + h) * p.per_head + (slot >> lbt);
+  const size_t v_scales = (size_t)p.Hkv * p.per_head;
+  float s_old[2] = {0.f, 0.f};
+  if (in_blk > 0) {
+    s_old[0] = sp[0];
+    s_old[1] = sp[v_scales];
+  }
+  auto max8 = [](uint4 v) {
+    return __vmaxu2(__vmaxu2(finite_abs2(v.x), finite_abs2(v.y)), __vmaxu2(finite_abs2(v.z), finite_abs2(v.w)));
+  };
+  const size_t side_bytes = (size_t)p.Hkv * ps * p.d_qk, page_bytes = side_bytes + (size_t)p.Hkv * ps * p.d_vo;
+#pragma unroll
+  for (int side = 0; side < 2; ++side) {
+    const int d = side ? p.d_vo : p.d_qk;
+    uint32_t m2 = __vmaxu2(max8(w[side][0]), max8(w[side][1]));
+    for (int r = 1; r < n; ++r) {
+      uint4 x[2];
+      load_row(side, i + r, x);
+      m2 = __vmaxu2(m2, __vmaxu2(max8(x[0]), max8(x[1])));
+    }
+    const uint32_t mb = __reduce_max_sync(0xffffffffu, max(m2 & 0xFFFFu, m2 >> 16));
+    const float s = fmaxf(s_old[side], __fmul_rn(__uint_as_float(mb << 16), KVT == KV_INT8B ? 1.f / 127.f : 1.f / 448.f));
+    const float r0 = s > 0.f ? fminf(__frcp_rn(s), 3.402823466e38f) : 0.f;
+    uint8_t* rows = p.cache + (size_t)page * page_bytes + (side ? side_bytes : 0) + ((size_t)h * ps + (slot - in_blk)) * d;
+    if (in_blk > 0 && s > s_old[side]) {
+      const float ratio = __fmul_rn(s_old[side], r0);
+      for (int u = lane; u < in_blk * (d / 16); u += 32) {
+        uint4* q = reinterpret_cast<uint4*>(rows) + u;
+        const uint4 c = *q;
+        *q = make_uint4(recode4<KVT>(c.x, ratio), recode4<KVT>(c.y, ratio), recode4<KVT>(c.z, ratio),
+                        recode4<KVT>(c.w, ratio));
+      }
+    }
+    if (lane == 0) sp[side * v_scales] = s;  // (every lane has read s_old: the maximum's exchange)
+    for (int r = 0; r < n; ++r) {
+      uint4 x[2] = {w[side][0], w[side][1]};
+      if (r > 0) load_row(side, i + r, x);
+      uint2* dst = reinterpret_cast<uint2*>(rows + (size_t)(in_blk + r) * d) + lane;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (k == 0 || d == 512)
+          dst[32 * k] = s > 0.f ? make_uint2(codes4w<KVT, true>(x[k].x, x[k].y, r0), codes4w<KVT, true>(x[k].z, x[k].w, r0))
+                                : make_uint2(0, 0);
+    }
   }
 }
 
@@ -498,13 +600,14 @@ int append_block_box_rows() { return kBoxRows; }
 template <int KVT>
 static cudaError_t run_append(const AppendBlockMaps& tm, const AppendBlockParams& p, int sms, cudaStream_t s) {
   const int bt = 1 << p.log2_tokens, d = std::max(p.d_qk, p.d_vo);
-  // Short appends (a decode step's: few new rows a sequence): a warp per row, so that every row
-  // starts at once.  Otherwise a block's worth of rows per group, among which about one block
-  // starts, and as many threads as keep a whole block in registers (64 elements each).
-  const bool steps = append_block_steps(p.total_new, p.batch);
-  const int tokens = steps ? 1 : bt;
+  if (append_block_steps(p.total_new, p.batch)) {
+    const long long grid = ((long long)p.total_new * p.Hkv + kStepWarps - 1) / kStepWarps;
+    if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
+    return launch_pdl(append_step_kernel<KVT>, dim3((unsigned)grid), dim3(32 * kStepWarps), 0, s, 1, p);
+  }
+  // A block's worth of rows per group of threads, among which about one block starts.
   int G = 32;
-  const long long units = ((long long)p.total_new + tokens - 1) / tokens * p.Hkv * 2;
+  const long long units = ((long long)p.total_new + bt - 1) / bt * p.Hkv * 2;
   // Streamed where a block is at least a box (8 tokens): G from 32 (8 x 256) to 256
   // threads (64 x 512)
   if (append_block_streams(p.total_new, p.batch, bt)) {
@@ -517,11 +620,11 @@ static cudaError_t run_append(const AppendBlockMaps& tm, const AppendBlockParams
     return launch_pdl(kern, dim3((unsigned)std::min<long long>(units, sms)), dim3(kConsumers + 32 * kProducers),
                       stages * stage, s, 1, tm, p, G, stages, stage, units);
   }
-  while (!steps && G * 16 * kRegs < d * bt) G *= 2;
+  while (G * 16 * kRegs < d * bt) G *= 2;  // the whole block in registers
   const int threads = G > 256 ? G : 256;
   const long long grid = (units + threads / G - 1) / (threads / G);
   if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
-  return launch_pdl(append_block_kernel<KVT>, dim3((unsigned)grid), dim3(threads), 0, s, 1, p, tokens, G);
+  return launch_pdl(append_block_kernel<KVT>, dim3((unsigned)grid), dim3(threads), 0, s, 1, p, G);
 }
 
 cudaError_t launch_append_block(int kvt, const AppendBlockMaps& tm, const AppendBlockParams& p, int sms,
