@@ -78,14 +78,17 @@ struct DecodeSmem {
 // exceeds target_chunks + batch (the workspace bound); each sequence's range is then
 // split evenly into ceil(pages / C) chunks.
 #ifdef PA_DECODE_AUX
-// Chunks for equal runs (p.shares > 0): with every sequence's visible pages laid one after the
-// other, a chunk ends at each sequence's end and at each multiple of S = ceil(total / shares)
-// pages (at least a tile of 64 tokens), so that every CTA streams the same number of pages (the last run may be short) and a
-// sequence is split only where a run ends inside it.  `total` is the visible pages.
+// Chunks for equal runs (p.shares > 0).  Every sequence with visible pages is laid out as `fixed`
+// units (what a chunk costs besides its pages, about 128 tokens' time) followed by its pages,
+// the sequences one after the other; run r is units [r S, (r + 1) S), S = ceil(all / shares)
+// (at least a tile of 64 tokens), and a chunk is what a run and a sequence's pages have in
+// common, so that every CTA has about the same to do and a sequence is split only where a run
+// ends inside it.  `total` is the visible pages.
 __device__ __forceinline__ void decode_plan_runs(const DecodeParams& p, int total, int* s_red) {
   __shared__ int s_pages, s_chunks;
   const int tid = threadIdx.x, ps = p.page_size;
-  const int S = max((total + p.shares - 1) / p.shares, max(1, 64 / ps));
+  const int fixed = max(1, 128 / ps);
+  int S = 1;
   // block-wide exclusive sums of v; `carry` runs over the rounds
   auto scan = [&](int v, int* carry) {
     const int own = v;
@@ -110,7 +113,17 @@ __device__ __forceinline__ void decode_plan_runs(const DecodeParams& p, int tota
     if (tid == (int)blockDim.x - 1) *carry = excl + own;
     return excl;
   };
+  // all units: the pages, and `fixed` for each sequence that has any
+  int some = 0;
+  for (int b = tid; b < p.batch; b += blockDim.x) some += p.kv_indptr[b + 1] > p.kv_indptr[b];
   if (tid == 0) s_pages = s_chunks = 0;
+  __syncthreads();
+  scan(some, &s_pages);
+  __syncthreads();
+  const long long all = total + (long long)fixed * s_pages;
+  S = (int)max((all + p.shares - 1) / p.shares, (long long)max(1, 64 / ps));
+  __syncthreads();
+  if (tid == 0) s_pages = 0;
   __syncthreads();
   for (int base = 0; base < p.batch; base += blockDim.x) {
     const int b = base + tid;
@@ -121,27 +134,29 @@ __device__ __forceinline__ void decode_plan_runs(const DecodeParams& p, int tota
         first = max(0, (np - 1) * ps + p.kv_last_page_len[b] - 1 - p.window_left) / ps;
     }
     const int pages = np - first;
-    const int e0 = scan(pages, &s_pages);  // the sequence's first page among all
+    const int start = scan(pages > 0 ? fixed + pages : 0, &s_pages);  // the sequence's first unit
+    const int e0 = start + fixed;                                     // its first page's
     const int n = pages > 0 ? (e0 + pages - 1) / S - e0 / S + 1 : 0;
     const int c0 = scan(n, &s_chunks);
     if (b < p.batch) {
       p.seq_info[b] = make_int2(c0, n);
       for (int k = 0; k < n; ++k) {
         const int run = e0 / S + k;
-        const int lo = max(e0, run * S), hi = min(e0 + pages, (run + 1) * S);
         DecodeChunk c;
         c.b = b;
-        c.page_begin = first + lo - e0;
-        c.page_end = first + hi - e0;
+        c.page_begin = first + max(e0, run * S) - e0;
+        c.page_end = first + min(e0 + pages, (run + 1) * S) - e0;
         c.split = k;
         p.chunks[c0 + k] = c;
-        if (lo == run * S) p.run_first[run] = c0 + k;
+        // the first chunk of this run, and of runs before it that hold none
+        for (int r = k > 0 ? run : (start > 0 ? (start - 1) / S + 1 : 0); r <= run; ++r) p.run_first[r] = c0 + k;
       }
     }
   }
   __syncthreads();
+  // runs behind the last page, and the end
   for (int r = tid; r <= p.shares; r += blockDim.x)
-    if (r * (long long)S >= total) p.run_first[r] = s_chunks;  // runs without pages, and the end
+    if (r * (long long)S >= s_pages) p.run_first[r] = s_chunks;
   if (tid == 0) {
     p.hdr[0] = s_chunks;
     p.hdr[1] = S;
@@ -152,6 +167,7 @@ __global__ void __launch_bounds__(1024) decode_plan_kernel(DecodeParams p) {
   __shared__ int s_red[32], s_max[32], s_min[32];
   __shared__ int s_carry;
   grid_dep_launch();  // the decode kernel may start its set-up (it waits for this grid)
+  grid_dep_wait();    // the work list may still be read by the call before
   const int tid = threadIdx.x;
   const int ps = p.page_size;
   // pass 1: total visible pages, and their largest and smallest count over the sequences
@@ -398,7 +414,8 @@ __device__ __forceinline__ void decode_merge_unit(const DecodeParams& p, int gw,
 template <int DVO>
 __global__ void __launch_bounds__(256) decode_merge_kernel(DecodeParams p) {
   constexpr int NQ = DVO / 128;  // column quarters (warps) per row
-  grid_dep_wait();  // the decode kernel's partials are complete
+  grid_dep_launch();  // the next call's kernel may start its set-up (it waits for this grid)
+  grid_dep_wait();    // the decode kernel's partials are complete
   const int lane = threadIdx.x & 31;
   const int units = p.batch * p.Hq * NQ;
   for (int gw = (blockIdx.x * blockDim.x + threadIdx.x) >> 5; gw < units; gw += (gridDim.x * blockDim.x) >> 5)

@@ -14,6 +14,7 @@ namespace pa {
 template <int KVT, int DQK, int DVO, bool COPY, bool PAD>
 __global__ void __launch_bounds__(1024) prefill_prep_kernel(const PrefillParams p, const DequantParams d) {
   grid_dep_launch();
+  grid_dep_wait();  // plan and copy may still be read by the call before
   if (blockIdx.x == 0) {
     prefill_plan_body(p);
     return;
@@ -24,18 +25,16 @@ __global__ void __launch_bounds__(1024) prefill_prep_kernel(const PrefillParams 
 template <int KVT, bool PAD>
 static cudaError_t run_prep(int dqk, int dvo, int grid, const PrefillParams& p, const DequantParams& d,
                             cudaStream_t s) {
-  if (dqk == 512 && dvo == 512) prefill_prep_kernel<KVT, 512, 512, true, PAD><<<grid, 1024, 0, s>>>(p, d);
-  else if (dqk == 512 && dvo == 256) prefill_prep_kernel<KVT, 512, 256, true, PAD><<<grid, 1024, 0, s>>>(p, d);
-  else if (dqk == 256 && dvo == 256) prefill_prep_kernel<KVT, 256, 256, true, PAD><<<grid, 1024, 0, s>>>(p, d);
-  else return cudaErrorInvalidValue;
-  return cudaGetLastError();
+  if (dqk == 512 && dvo == 512) return launch_pdl(prefill_prep_kernel<KVT, 512, 512, true, PAD>, dim3(grid), dim3(1024), 0, s, 1, p, d);
+  if (dqk == 512 && dvo == 256) return launch_pdl(prefill_prep_kernel<KVT, 512, 256, true, PAD>, dim3(grid), dim3(1024), 0, s, 1, p, d);
+  if (dqk == 256 && dvo == 256) return launch_pdl(prefill_prep_kernel<KVT, 256, 256, true, PAD>, dim3(grid), dim3(1024), 0, s, 1, p, d);
+  return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_prefill_prep(int kvt, int dqk, int dvo, int copy, const PrefillParams& p,
                                 const DequantParams& d, int sms, cudaStream_t s) {
   if (copy == 0) {
-    prefill_prep_kernel<KV_BF16, 512, 512, false, false><<<1, 1024, 0, s>>>(p, d);
-    return cudaGetLastError();
+    return launch_pdl(prefill_prep_kernel<KV_BF16, 512, 512, false, false>, dim3(1), dim3(1024), 0, s, 1, p, d);
   }
   // two 1024-thread blocks per SM, the planner's among them, all resident at once (one
   // block more would wait for a slot and run as a second wave)

@@ -295,10 +295,16 @@ __device__ __forceinline__ void prefill_plan_body(const PrefillParams& p) {
     // least 4 KV tiles a part.  (Chunks of one fixed size rounded each range's part
     // count up: 4 x 32 new tokens over 16384 keys gave 320 items of 13 tiles, a third
     // round for 16 CTAs.)
+    // (Block scales: parts of a single KV tile where every item then has a CTA of its own;
+    // a few new tokens over some hundred otherwise wait for several tiles one after another:
+    // 4 x 4 new tokens over up to 737, 4 kv heads, 51 -> 40 us.)
+    const long long visits = total * p.Hkv;  // tiles of all items
+    const bool fine = p.bs.s != nullptr && visits <= 4ll * p.split_target;
+    const int least = fine ? 1 : 4;
     if (tid < n_tiles) {
       const int nt = t_nt[tid];
-      const long long want = (long long)nt * 2 * p.split_target / max(1ll, total * p.Hkv);
-      const int parts = (int)max(1ll, min((long long)(nt + 3) / 4, want));
+      const long long want = (long long)nt * (fine ? 1 : 2) * p.split_target / max(1ll, visits);
+      const int parts = (int)max(1ll, min((long long)(nt + least - 1) / least, want));
       // as many parts as parts of ceil(nt / parts) tiles need: none comes out empty
       // (25 tiles in 6 parts of 5 would leave the sixth empty)
       const int step = (nt + parts - 1) / parts;
