@@ -15,8 +15,9 @@
 //
 // Bytes: 2 read and 1 written per element, plus a scale per block.  A group of threads takes
 // one (block, kv head, side): it finds its new rows' largest magnitude, then writes the codes.
-// Short appends and blocks of 1 to 4 tokens load the rows into registers
-// (append_block_kernel), the others stream them through shared memory (append_stream_kernel).
+// Short appends take a warp per row and head (append_step_kernel); long ones stream the rows
+// through shared memory (append_stream_kernel), or, in blocks of two or four tokens, load them
+// into registers (append_block_kernel).
 #include <algorithm>
 
 #include "launch.h"
@@ -90,7 +91,7 @@ __device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio) {
 constexpr int kStepWarps = 8;  // warps per CTA of append_step_kernel
 constexpr int kRegs = 4;  // 16-element pieces of a block's new rows that a thread keeps
 
-// Long appends in blocks of fewer tokens than a TMA box.  A group of G threads (a power of two,
+// Long appends in blocks of two or four tokens, fewer than a TMA box.  A group of G threads (a power of two,
 // at least a warp) takes the blocks whose first new row lies among a block's worth of
 // consecutive new rows, for one kv head and side; blockDim.x / G groups per CTA.
 template <int KVT>
@@ -245,8 +246,8 @@ __global__ void __launch_bounds__(512, 2) append_block_kernel(const AppendBlockP
 }
 
 // ---------------------------------------------------------------------------------------
-// Short appends (a decode step's, few new rows a sequence): a warp per (new row, kv head), K and
-// V together.  What takes time is the chain of dependent loads, so the row's values are loaded
+// Short appends (a decode step's, few new rows a sequence) and blocks of one token: a warp per
+// (new row, kv head), K and V together.  What takes time is the chain of dependent loads, so the row's values are loaded
 // at once, beside the guess that row i belongs to sequence i; then the page id, then the old
 // scales.  A warp whose row is not its block's first new one leaves; one whose block has more
 // new rows reads those too.
@@ -600,7 +601,9 @@ int append_block_box_rows() { return kBoxRows; }
 template <int KVT>
 static cudaError_t run_append(const AppendBlockMaps& tm, const AppendBlockParams& p, int sms, cudaStream_t s) {
   const int bt = 1 << p.log2_tokens, d = std::max(p.d_qk, p.d_vo);
-  if (append_block_steps(p.total_new, p.batch)) {
+  // (Blocks of one token too: 19 thousand rows of 4 x (256 + 256) 47 us in groups, 27 us in
+  // warps; blocks of four, 84 rows for each of 88 sequences, 18 and 30 us.)
+  if (append_block_steps(p.total_new, p.batch) || bt == 1) {
     const long long grid = ((long long)p.total_new * p.Hkv + kStepWarps - 1) / kStepWarps;
     if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
     return launch_pdl(append_step_kernel<KVT>, dim3((unsigned)grid), dim3(32 * kStepWarps), 0, s, 1, p);

@@ -10,6 +10,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -35,10 +36,20 @@ const at::Tensor* tensor(PyObject* o) {
   return &THPVariable_Unpack(o);
 }
 
+thread_local int g_device = -1;  // the current device as this call has seen it, -1: not asked yet
+
+void check_device(const at::Tensor& t) {
+  if (!t.is_cuda()) bad(PyExc_ValueError, "tensor arguments must be CUDA tensors");
+  // the library launches on the current device, whose kernels may not reach another's memory
+  if (g_device < 0) g_device = c10::cuda::current_device();
+  if (t.get_device() != g_device)
+    bad(PyExc_ValueError, "tensor arguments must live on the current CUDA device");
+}
+
 // The device address of a contiguous CUDA tensor, null for None.
 void* pointer(const at::Tensor* t) {
   if (!t) return nullptr;
-  if (!t->is_cuda()) bad(PyExc_ValueError, "tensor arguments must be CUDA tensors");
+  check_device(*t);
   if (!t->is_contiguous()) bad(PyExc_ValueError, "tensor arguments must be contiguous");
   return t->data_ptr();
 }
@@ -189,6 +200,7 @@ PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F f) {
     PyErr_Format(PyExc_TypeError, "expected %zd arguments, got %zd", want, n);
     return nullptr;
   }
+  g_device = -1;
   try {
     return f();
   } catch (const BadArgument&) {
@@ -296,7 +308,7 @@ struct Table {
 // An int32 block table whose rows are contiguous.
 Table table_of(PyObject* o) {
   const at::Tensor* t = tensor(o);
-  if (t && !t->is_cuda()) bad(PyExc_ValueError, "tensor arguments must be CUDA tensors");
+  if (t) check_device(*t);
   if (!t || t->scalar_type() != at::kInt || t->dim() != 2 || (t->size(1) > 1 && t->stride(1) != 1))
     bad(PyExc_ValueError, "block_table must be int32 [rows, max_pages] with contiguous rows");
   return {static_cast<int32_t*>(t->data_ptr()), int_of(t->size(0)), int_of(t->size(1)),

@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(DecodeCfg<KVT, DQK, DVO>::THREADS, 1)
     if (warp == 9) {
       // ---------------------------------------------------------------- block scales
       // The K and V scale of each token of a tile into the tile's stage (0 past the end of
-      // the sequence), two tokens per lane, and the tile's largest V scale.  Page ids are
+      // the sequence and before the window, whatever the pool holds there), two tokens per lane, and the tile's largest V scale.  Page ids are
       // fetched two tiles ahead and scales one tile ahead of the wait for the stage, so the
       // two dependent loads behind a scale are off the consumers' path.
       float* sc0 = reinterpret_cast<float*>(smem + L::OFF_SC);
@@ -596,13 +596,14 @@ __global__ void __launch_bounds__(DecodeCfg<KVT, DQK, DVO>::THREADS, 1)
         const int np = p.kv_indptr[ch.b + 1] - ip0;
         const int kv_len = (np - 1) * ps + p.kv_last_page_len[ch.b];
         const int tok_end = min(ch.page_end * ps, kv_len);
+        const int win_lo = p.window_left >= 0 ? kv_len - 1 - p.window_left : 0;
         int page[T / 32];
         float ks[T / 32], vs[T / 32];
         auto load_pages = [&](int tok0) {
 #pragma unroll
           for (int k = 0; k < T / 32; ++k) {
             const int tok = tok0 + lane + 32 * k;
-            page[k] = tok < tok_end ? __ldg(p.kv_indices + ip0 + (tok >> lps)) : -1;
+            page[k] = tok < tok_end && tok >= win_lo ? __ldg(p.kv_indices + ip0 + (tok >> lps)) : -1;
           }
         };
         auto load_scales = [&](int tok0) {

@@ -1443,10 +1443,15 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DVO, KVT, PAIR, SC>::THREADS, 
     uint32_t* vm_s = reinterpret_cast<uint32_t*>(ks_s + 256);
     constexpr int kMinVeb = 6;  // the power of two stays a normal float
     int veb = kMinVeb;
-    auto sc_page = [&](const PrefillItemInfo& f, int tile) -> int {  // page of this thread's row, -1: no token
+    // page of this thread's row of a tile; -1 (scales 0): no token, or before every query's
+    // window, whatever the pool holds there
+    auto sc_page = [&](const PrefillItemInfo& f, int tile) -> int {
       const int pg = tile * (128 / p.box_rows) + row / p.box_rows, slot = row % p.box_rows;
-      if (slot >= ps || pg >= f.np || pg * ps + slot >= f.kv_len) return -1;
-      return __ldg(p.kv_indices + f.ip0 + pg);
+      const int key = pg * ps + slot;
+      if (slot >= ps || pg >= f.np || key >= f.kv_len) return -1;
+      if (p.window_left >= 0 && key < f.pos0 - p.window_left) return -1;
+      const int page = __ldg(p.kv_indices + f.ip0 + pg);
+      return page < p.num_pages ? page : -1;
     };
     auto sc_load = [&](const PrefillItemInfo& f, int page, float& k, float& v) {
       k = v = 0.f;

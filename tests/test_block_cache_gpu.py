@@ -381,6 +381,47 @@ def test_prefill_v_scales_over_the_whole_float_range(shape, order):
         ref.check(out, lse, want, f"limit {limit}")
 
 
+@pytest.mark.parametrize("phase", ["decode", "prefill"])
+def test_scales_before_the_window_are_not_used(phase):
+    """NaN scales in blocks wholly before every query's window, in pages that hold visible
+    tokens and in others."""
+    new = [1, 1] if phase == "decode" else [9, 40]
+    c = ref.make(fmt=INT8, kv_lens=[500, 290], qo_lens=new, Hkv=2, group=4, page_size=64, bt=8, seed=83, window_left=90)
+    want = ref.attend(c, c.cache, c.scales)
+    for b, (L, n) in enumerate(zip(c.kv_lens, new)):
+        lo = L - n - 90  # the first visible token
+        for i in range(lo // 8):  # blocks before it
+            c.scales[c.kv_indices[c.kv_indptr[b] + i * 8 // 64], :, :, i * 8 % 64 // 8] = np.nan
+    for limit in (-1, 0):
+        pa.paged_attn_set_prefill_dequant_limit(limit)
+        try:
+            out, lse = decode(c) if phase == "decode" else prefill(c)
+        finally:
+            pa.paged_attn_set_prefill_dequant_limit(-1)
+        ref.check(out, lse, want, f"limit {limit}")
+
+
+def test_given_outputs_and_stream():
+    """out, lse and stream arguments: written in place, on that stream."""
+    c = ref.make(fmt=FP8, kv_lens=[300, 41], qo_lens=[20, 41], n_new=[5, 41], Hkv=2, group=3, page_size=16, bt=8, seed=84)
+    side = torch.cuda.Stream()
+    cache, scales = gpu(c.cache), gpu(c.scales)
+    args = [gpu(x) for x in (c.kv_indptr, c.kv_indices, c.last)]
+    k, v, ai, q, qi = (gpu(x) for x in (c.k_new, c.v_new, c.append_indptr, c.q, c.qo_indptr))
+    out = torch.empty(61, 6, 512, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(61, 6, device="cuda")
+    torch.cuda.synchronize()
+    pa.paged_attn_append_kv_block(k, v, ai, cache, *args, scales, page_size=16, block_tokens=8, kv_dtype=FP8, stream=side)
+    got = pa.paged_attn_prefill(q, qi, cache, *args, out=out, lse=lse, stream=side, block_scales=scales, **kwargs(c))
+    assert got[0] is out and got[1] is lse
+    side.synchronize()
+    after = ref.append(c, c.cache, c.scales)
+    assert np.array_equal(cache.cpu().numpy(), after[0])
+    ref.check(out, lse, ref.attend(c, *after))
+    out2, none = pa.paged_attn_decode(q[:2], cache, *args, return_lse=False, block_scales=scales, **kwargs(c))
+    assert none is None and out2.shape == (2, 6, 512)
+
+
 def test_prefill_longer_than_the_probability_scratch():
     """More than 64 KV tiles: head_dim_vo 512 recomputes the scores in its second pass."""
     c = ref.make(fmt=INT8, kv_lens=[8400], qo_lens=[6], Hkv=1, group=4, page_size=64, bt=64, seed=82)
