@@ -99,8 +99,8 @@ __global__ void __launch_bounds__(512, 2) append_block_kernel(const AppendBlockP
   __shared__ uint32_t s_max[2][32];  // per warp, in turn: the largest magnitude
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int group = threadIdx.x / G, tid = threadIdx.x & (G - 1);
-  grid_dep_launch();  // the next call's kernel may start its set-up (it waits for this grid)
   grid_dep_wait();
+  grid_dep_launch();  // the next call's kernel may start its set-up (it waits for this grid)
   const long long unit = (long long)blockIdx.x * (blockDim.x / G) + group;
   const bool is_v = unit & 1;
   const int h = (int)((unit >> 1) % p.Hkv);
@@ -255,8 +255,8 @@ template <int KVT>
 __global__ void __launch_bounds__(32 * kStepWarps, 4) append_step_kernel(const AppendBlockParams p) {
   const int lane = threadIdx.x & 31;
   const long long unit = (long long)blockIdx.x * kStepWarps + (threadIdx.x >> 5);
-  grid_dep_launch();  // the next call's kernel may start its set-up (it waits for this grid)
   grid_dep_wait();
+  grid_dep_launch();  // the next call's kernel may start its set-up (it waits for this grid)
   const int h = (int)(unit % p.Hkv);
   if (unit / p.Hkv >= p.total_new) return;
   const int i = (int)(unit / p.Hkv);

@@ -166,8 +166,8 @@ __device__ __forceinline__ void decode_plan_runs(const DecodeParams& p, int tota
 __global__ void __launch_bounds__(1024) decode_plan_kernel(DecodeParams p) {
   __shared__ int s_red[32], s_max[32], s_min[32];
   __shared__ int s_carry;
-  grid_dep_launch();  // the decode kernel may start its set-up (it waits for this grid)
   grid_dep_wait();    // the work list may still be read by the call before
+  grid_dep_launch();  // the decode kernel may start its set-up (it waits for this grid)
   const int tid = threadIdx.x;
   const int ps = p.page_size;
   // pass 1: total visible pages, and their largest and smallest count over the sequences
@@ -414,8 +414,8 @@ __device__ __forceinline__ void decode_merge_unit(const DecodeParams& p, int gw,
 template <int DVO>
 __global__ void __launch_bounds__(256) decode_merge_kernel(DecodeParams p) {
   constexpr int NQ = DVO / 128;  // column quarters (warps) per row
-  grid_dep_launch();  // the next call's kernel may start its set-up (it waits for this grid)
   grid_dep_wait();    // the decode kernel's partials are complete
+  grid_dep_launch();  // the next call's kernel may start its set-up (it waits for this grid)
   const int lane = threadIdx.x & 31;
   const int units = p.batch * p.Hq * NQ;
   for (int gw = (blockIdx.x * blockDim.x + threadIdx.x) >> 5; gw < units; gw += (gridDim.x * blockDim.x) >> 5)

@@ -13,8 +13,8 @@ namespace pa {
 // grid before it reads either result.
 template <int KVT, int DQK, int DVO, bool COPY, bool PAD>
 __global__ void __launch_bounds__(1024) prefill_prep_kernel(const PrefillParams p, const DequantParams d) {
-  grid_dep_launch();
   grid_dep_wait();  // plan and copy may still be read by the call before
+  grid_dep_launch();
   if (blockIdx.x == 0) {
     prefill_plan_body(p);
     return;

@@ -22,8 +22,8 @@ template <int DVO>
 __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillParams p) {
   constexpr int G4 = DVO / 128;  // float4 groups per lane
   constexpr int B = 4;           // parts loaded together
-  grid_dep_launch();  // the next call's kernel may start its set-up (it waits for this grid)
   grid_dep_wait();    // the prefill kernel's partial slots are complete
+  grid_dep_launch();  // the next call's kernel may start its set-up (it waits for this grid)
   const int n = p.hdr[1];
   const int g = p.group;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

@@ -105,8 +105,8 @@ __global__ void __launch_bounds__(kT, 1) resize_kernel(const ResizeParams p) {
   __shared__ ScanWords s_w;
   __shared__ long long s_l[32];
   const int tid = threadIdx.x, part = blockIdx.x, parts = gridDim.x;
-  grid_dep_launch();  // the next call's kernel may start its set-up (it waits for this grid)
   grid_dep_wait();
+  grid_dep_launch();  // the next call's kernel may start its set-up (it waits for this grid)
   const long long count = *p.free_count;
   const Change c0 = change_of(p, tid);
   const bool one_round = p.batch <= kT;
@@ -209,8 +209,8 @@ __global__ void __launch_bounds__(kT, 1) build_kernel(const BuildParams p) {
   __shared__ ScanWords s_w;
   __shared__ long long s_l[32];
   const int tid = threadIdx.x, ps = 1 << p.log2_page;
-  grid_dep_launch();
   grid_dep_wait();
+  grid_dep_launch();
   const Listed l0 = listed_of(p, tid);
   const bool one_round = p.batch <= kT;
   long long pages = l0.pages, tokens = l0.fresh;
