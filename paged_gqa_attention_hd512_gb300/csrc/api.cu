@@ -701,12 +701,18 @@ int prefill_call(const void* q, const int32_t* qo_indptr, int total_q, const voi
   // FP8 / NVFP4 / 8-bit codes with block scales: convert the referenced pages once into a
   // 16-bit copy and run the bf16 kernel on it, when the copy fits the limit; else convert
   // inside the kernel
-  const bool quant = kv_dtype != PA_KV_BF16;
+  const bool quant = kv_dtype != PA_KV_BF16, scaled = kv_block_scaled(kv_dtype);
   const uint64_t bf16_page = (uint64_t)num_kv_heads * rows_copy * (head_dim_qk + head_dim_vo) * 2;
-  const bool dequant = (quant || pad) && (uint64_t)num_pages * bf16_page <= g_prefill_dequant_limit.load();
+  // Codes with block scales are converted in the kernel where the batch has at most a query
+  // tile a sequence: each KV tile is then converted once, and the copy (a byte read, two
+  // written and two read again per element) only costs.  4 sequences of 16384 tokens with 4
+  // new ones, 2 kv heads of 512 / 256: copy 97 us, in the kernel 65; with 32 new ones (two
+  // tiles) 119 and 117, with 64 179 and 228; head_dim_vo 512 (two passes): 133 and 120, 174
+  // and 232, 266 and 457.
+  const bool one_tile = scaled && !pad && total_q <= (long long)batch * rows_per_tile;
+  const bool dequant = (quant || pad) && !one_tile && (uint64_t)num_pages * bf16_page <= g_prefill_dequant_limit.load();
   if (pad && !dequant) return PA_ERR_UNSUPPORTED;  // the padded copy would exceed the limit
   const int run_kvt = dequant ? (int)PA_KV_BF16 : kv_dtype;
-  const bool scaled = kv_block_scaled(kv_dtype);
   const int smem = scaled ? prefill_block_smem_bytes(run_kvt, head_dim_qk, head_dim_vo)
                           : prefill_smem_bytes(run_kvt, head_dim_qk, head_dim_vo);
   if (smem > smem_optin) return PA_ERR_SMEM;

@@ -299,11 +299,14 @@ __device__ __forceinline__ void prefill_plan_body(const PrefillParams& p) {
     // a few new tokens over some hundred otherwise wait for several tiles one after another:
     // 4 x 4 new tokens over up to 737, 4 kv heads, 51 -> 40 us.)
     const long long visits = total * p.Hkv;  // tiles of all items
-    const bool fine = p.bs.s != nullptr && visits <= 4ll * p.split_target;
-    const int least = fine ? 1 : 4;
+    const int least = p.bs.s != nullptr && visits <= 4ll * p.split_target ? 1 : 4;
+    // (Block scales: one round of items, whose Q tile and partial rows then move once: 4 x 32
+    // new tokens over 16384, 2 kv heads of 512 / 256, 125 -> 120 us, 8 x 32 over 3000 to 8000
+    // 92 -> 85 us.  The other dtypes keep two.)
+    const int rounds = p.bs.s != nullptr ? 1 : 2;
     if (tid < n_tiles) {
       const int nt = t_nt[tid];
-      const long long want = (long long)nt * (fine ? 1 : 2) * p.split_target / max(1ll, visits);
+      const long long want = (long long)nt * rounds * p.split_target / max(1ll, visits);
       const int parts = (int)max(1ll, min((long long)(nt + least - 1) / least, want));
       // as many parts as parts of ceil(nt / parts) tiles need: none comes out empty
       // (25 tiles in 6 parts of 5 would leave the sixth empty)
