@@ -634,6 +634,7 @@ int paged_attn_decode(const void* q, const void* kv_cache, const int32_t* kv_ind
   p.chunks = reinterpret_cast<DecodeChunk*>(ws + o_chunks);
   p.seq_info = reinterpret_cast<int2*>(ws + o_seq);
   p.shares = shares;
+  p.find_runs = shares > 0 && batch <= decode_run_list() ? 1 : 0;
   p.run_first = reinterpret_cast<int*>(ws + o_run);
   p.ws_ml = reinterpret_cast<float2*>(ws + o_ml);
   p.ws_o = reinterpret_cast<float*>(ws + o_o);
@@ -656,7 +657,7 @@ int paged_attn_decode(const void* q, const void* kv_cache, const int32_t* kv_ind
   L.grid = grid;
   L.stream = static_cast<cudaStream_t>(stream);
 
-  if (!direct && launch_decode_plan(p, L.stream) != cudaSuccess) return PA_ERR_CUDA;
+  if (!direct && !p.find_runs && launch_decode_plan(p, L.stream) != cudaSuccess) return PA_ERR_CUDA;
   const char* name = "?";
   cudaError_t e;
   prof_mark(L.stream, true);
@@ -1174,6 +1175,7 @@ extern "C" int paged_attn_decode_noalloc(const void* q, const void* kv_cache, co
   p.chunks = reinterpret_cast<DecodeChunk*>(ws + o_chunks);
   p.seq_info = reinterpret_cast<int2*>(ws + o_seq);
   p.shares = shares;
+  p.find_runs = shares > 0 && batch <= decode_run_list() ? 1 : 0;
   p.run_first = reinterpret_cast<int*>(ws + o_run);
   p.ws_ml = reinterpret_cast<float2*>(ws + o_ml);
   p.ws_o = reinterpret_cast<float*>(ws + o_o);
@@ -1194,7 +1196,7 @@ extern "C" int paged_attn_decode_noalloc(const void* q, const void* kv_cache, co
   p.direct = direct ? 1 : 0;
   p.sm_scale = sm_scale;
 
-  if (!direct && launch_decode_plan(p, L.stream) != cudaSuccess) return PA_ERR_CUDA;
+  if (!direct && !p.find_runs && launch_decode_plan(p, L.stream) != cudaSuccess) return PA_ERR_CUDA;
   const char* name = "?";
   cudaError_t e;
   prof_mark(L.stream, true);

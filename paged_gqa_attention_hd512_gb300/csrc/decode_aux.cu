@@ -32,6 +32,8 @@ int decode_smem_bytes(int kvt, int dqk, int dvo, int hp) {
   return smem_of<KV_NVFP4>(dqk, dvo, hp);
 }
 
+int decode_run_list() { return kRunList; }
+
 int decode_tile_tokens(int kvt, int dqk) {
   return (kvt == KV_BF16 && dqk == 512) ? 32 : 64;
 }

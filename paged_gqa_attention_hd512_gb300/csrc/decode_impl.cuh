@@ -54,6 +54,8 @@ struct DecodeCfg {
   static_assert(NS >= 2, "ring too shallow");
 };
 
+constexpr int kRunList = 512;  // chunks of a CTA's run, at most one for each sequence
+
 template <int KVT, int DQK, int DVO, int HP>
 struct DecodeSmem {
   using C = DecodeCfg<KVT, DQK, DVO>;
@@ -66,7 +68,9 @@ struct DecodeSmem {
   static constexpr int OFF_ML = OFF_ALPHA + HP * 4;
   static constexpr int OFF_QMAX = OFF_ML + HP * 8;
   static constexpr int OFF_SC = (OFF_QMAX + 8 * 4 + 15) / 16 * 16;
-  static constexpr int OFF_BAR = OFF_SC + C::NS * C::SC_STAGE * 4;
+  // block-scaled codes: the CTA's chunks (decode_runs_of_cta) and the scratch of finding them
+  static constexpr int OFF_LIST = OFF_SC + C::NS * C::SC_STAGE * 4;
+  static constexpr int OFF_BAR = OFF_LIST + (C::BLK ? kRunList * 16 + 64 * 4 : 0);
   static constexpr int BYTES = OFF_BAR + 2 * C::NS * 8;
   static constexpr int ALLOC = BYTES + 1024;  // slack to align the base to 1024 bytes
 };
@@ -414,8 +418,10 @@ __device__ __forceinline__ void decode_merge_unit(const DecodeParams& p, int gw,
 template <int DVO>
 __global__ void __launch_bounds__(256) decode_merge_kernel(DecodeParams p) {
   constexpr int NQ = DVO / 128;  // column quarters (warps) per row
-  grid_dep_wait();    // the decode kernel's partials are complete
-  grid_dep_launch();  // the next call's kernel may start its set-up (it waits for this grid)
+  grid_dep_wait();  // the decode kernel's partials are complete
+  // the next call's planner may start its set-up (it waits for this grid); a decode kernel that
+  // finds its own runs would take the SMs from a merge of several blocks each
+  if (!p.find_runs || gridDim.x <= (unsigned)p.grid) grid_dep_launch();
   const int lane = threadIdx.x & 31;
   const int units = p.batch * p.Hq * NQ;
   for (int gw = (blockIdx.x * blockDim.x + threadIdx.x) >> 5; gw < units; gw += (gridDim.x * blockDim.x) >> 5)
@@ -479,6 +485,78 @@ __device__ __forceinline__ void fp4_vt_pairs(uint32_t r, uint32_t* f) {
   e2m1x8_to_f16x2x4(ta | (tb << 4), f);        // byte e = (t_a, t_b) at column e
 }
 
+// The chunks of run `run` (see decode_plan_runs), found by the CTA itself: a launch and the
+// loads of a work list less.  Every CTA goes over the whole batch (at most kRunList
+// sequences); one of them records seq_info for the merge.  list: {sequence, first page, last
+// page + 1, 2 x partial row + (1: the sequence's only chunk)}; returns their number.
+template <int THREADS>
+__device__ __forceinline__ int decode_runs_of_cta(const DecodeParams& p, int run, bool record, int4* list,
+                                                  int* scratch) {
+  constexpr int NW = THREADS / 32;
+  static_assert(NW <= 16, "scratch");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, ps = p.page_size;
+  const int fixed = max(1, 128 / ps);
+  auto visible = [&](int b, int& first) -> int {
+    first = 0;
+    if (b >= p.batch) return 0;
+    const int np = max(0, __ldg(p.kv_indptr + b + 1) - __ldg(p.kv_indptr + b));
+    if (np > 0 && p.window_left >= 0)
+      first = max(0, (np - 1) * ps + __ldg(p.kv_last_page_len + b) - 1 - p.window_left) / ps;
+    return np - first;
+  };
+  int units = 0;
+  for (int b = tid; b < p.batch; b += THREADS) {
+    int first;
+    const int pages = visible(b, first);
+    if (pages > 0) units += fixed + pages;
+  }
+  for (int o = 16; o > 0; o >>= 1) units += __shfl_xor_sync(0xffffffffu, units, o);
+  if (lane == 0) scratch[warp] = units;
+  if (tid == 0) scratch[48] = 0;
+  __syncthreads();
+  long long all = 0;
+  for (int w = 0; w < NW; ++w) all += scratch[w];
+  const int S = (int)max((all + p.shares - 1) / p.shares, (long long)max(1, 64 / ps));
+  int unit0 = 0, chunk0 = 0;
+  // exclusive block-wide sum of v (words at `w`), and the total
+  auto scan = [&](int v, int* w, int& total) {
+    int incl = v;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    if (lane == 31) w[warp] = incl;
+    __syncthreads();
+    int before = 0;
+    total = 0;
+    for (int k = 0; k < NW; ++k) {
+      const int t = w[k];
+      if (k < warp) before += t;
+      total += t;
+    }
+    return before + incl - v;
+  };
+  for (int base = 0; base < p.batch; base += THREADS) {
+    const int b = base + tid;
+    int first, all_units, all_chunks;
+    const int pages = visible(b, first);
+    const int e0 = unit0 + scan(pages > 0 ? fixed + pages : 0, scratch + 16, all_units) + fixed;
+    const int n = pages > 0 ? (e0 + pages - 1) / S - e0 / S + 1 : 0;
+    const int c0 = chunk0 + scan(n, scratch + 32, all_chunks);
+    if (record && b < p.batch) p.seq_info[b] = make_int2(c0, n);
+    const int k = run - e0 / S;
+    if (k >= 0 && k < n)
+      list[atomicAdd(scratch + 48, 1)] = make_int4(b, first + max(e0, run * S) - e0, first + min(e0 + pages, (run + 1) * S) - e0,
+                                                   2 * (c0 + k) + (n == 1 ? 1 : 0));
+    unit0 += all_units;
+    chunk0 += all_chunks;
+    __syncthreads();  // the words may be written again
+  }
+  // runs of some hundred tokens: the merge may be launched at once (it waits for this grid)
+  if (S * (long long)ps <= 1024) grid_dep_launch();
+  return scratch[48];
+}
+
 // Bytes A and B (0..3) of r as an f16 pair, A in the low half; exact for both code types.
 template <int KVT, int A, int B>
 __device__ __forceinline__ uint32_t b8_pair_f16x2(uint32_t r) {
@@ -519,19 +597,35 @@ __global__ void __launch_bounds__(DecodeCfg<KVT, DQK, DVO>::THREADS, 1)
   __syncthreads();
   grid_dep_wait();  // the planner of this call is complete
   // this CTA's items: it0, it0 + step, ... below n_items
-  int n_items = p.direct ? p.batch * p.Hkv : p.hdr[0] * p.Hkv;
+  int n_items = p.direct ? p.batch * p.Hkv : (C::BLK && p.find_runs) ? 0 : p.hdr[0] * p.Hkv;
   int it0 = blockIdx.x, step = gridDim.x;
+  const int4* my_list = reinterpret_cast<const int4*>(smem + L::OFF_LIST);
   if constexpr (C::BLK) {
     if (!p.direct && p.shares > 0) {
       const int run = blockIdx.x / p.Hkv;
       step = p.Hkv;
       it0 = n_items = 0;
-      if (run < p.shares) {
+      if (p.find_runs) {
+        it0 = blockIdx.x % p.Hkv;
+        const int n = decode_runs_of_cta<C::THREADS>(p, run, blockIdx.x == 0, reinterpret_cast<int4*>(smem + L::OFF_LIST),
+                                                     reinterpret_cast<int*>(smem + L::OFF_LIST + kRunList * 16));
+        n_items = run < p.shares ? n * p.Hkv : 0;
+      } else if (run < p.shares) {
         it0 = p.run_first[run] * p.Hkv + blockIdx.x % p.Hkv;
         n_items = p.run_first[run + 1] * p.Hkv;
       }
     }
   }
+  // item it's chunk
+  auto item_chunk = [&](int it) -> DecodeChunk {
+    if constexpr (C::BLK) {
+      if (!p.direct && p.find_runs) {
+        const int4 r = my_list[it / p.Hkv];
+        return {r.x, r.y, r.z, r.w};
+      }
+    }
+    return decode_item_chunk(p, it);
+  };
   const int ps = p.page_size;
 
   if (warp == 8) {
@@ -546,7 +640,7 @@ __global__ void __launch_bounds__(DecodeCfg<KVT, DQK, DVO>::THREADS, 1)
     const int br = p.box_rows;
     uint32_t g = 0;
     for (int it = it0; it < n_items; it += step) {
-      const DecodeChunk ch = decode_item_chunk(p, it);
+      const DecodeChunk ch = item_chunk(it);
       const int kvh = it % p.Hkv;
       const int ip0 = p.kv_indptr[ch.b];
       const int np = p.kv_indptr[ch.b + 1] - ip0;
@@ -590,7 +684,7 @@ __global__ void __launch_bounds__(DecodeCfg<KVT, DQK, DVO>::THREADS, 1)
       const int lps = 31 - __clz(ps);
       uint32_t g = 0;
       for (int it = it0; it < n_items; it += step) {
-        const DecodeChunk ch = decode_item_chunk(p, it);
+        const DecodeChunk ch = item_chunk(it);
         const int kvh = it % p.Hkv;
         const int ip0 = p.kv_indptr[ch.b];
         const int np = p.kv_indptr[ch.b + 1] - ip0;
@@ -667,7 +761,7 @@ __global__ void __launch_bounds__(DecodeCfg<KVT, DQK, DVO>::THREADS, 1)
   uint32_t g = 0;
 
   for (int it = it0; it < n_items; it += step) {
-    const DecodeChunk ch = decode_item_chunk(p, it);
+    const DecodeChunk ch = item_chunk(it);
     const int kvh = it % p.Hkv;
     const int b = ch.b;
     const int ip0 = p.kv_indptr[b];
@@ -1007,11 +1101,13 @@ __global__ void __launch_bounds__(DecodeCfg<KVT, DQK, DVO>::THREADS, 1)
 
     // ---- epilogue: the final row (single chunk) or a partial (O, m, l)
     // (a direct item without a visible key wrote no (m, l): its row is 0, its lse -inf)
-    const int2 si = p.direct ? make_int2(0, 1) : p.seq_info[b];
+    // (found runs: the chunk's record has its partial row and whether it is the only one)
+    const bool found = C::BLK && !p.direct && p.find_runs;
+    const int2 si = p.direct ? make_int2(0, 1) : found ? make_int2(0, ch.split & 1) : p.seq_info[b];
     const bool direct = (si.y == 1);
     const bool keys = n_tiles > 0;
     if constexpr (C::BLK) vscale = __uint_as_float((uint32_t)(veb - 13) << 23);  // 2^(veb - 140)
-    const size_t prow = (size_t)(si.x + ch.split);
+    const size_t prow = (size_t)(found ? ch.split >> 1 : si.x + ch.split);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

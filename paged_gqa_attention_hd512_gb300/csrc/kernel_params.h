@@ -79,6 +79,7 @@ struct DecodeParams {
   // [run_first[r], run_first[r + 1])
   int shares;
   int* run_first;  // [shares + 1]
+  int find_runs;   // 1: each CTA finds its run itself (no planner, run_first unused)
 };
 
 // Prefill work item: one tile of query rows (positions x heads of one kv head).

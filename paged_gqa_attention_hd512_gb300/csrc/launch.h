@@ -80,6 +80,8 @@ cudaError_t launch_decode_plan(const DecodeParams& p, cudaStream_t s);
 cudaError_t launch_decode_merge(int dvo, const DecodeParams& p, int sms, cudaStream_t s);
 // Shared memory (bytes) the decode kernel of this shape needs.
 int decode_smem_bytes(int kvt, int dqk, int dvo, int hp);
+// Sequences of a batch whose runs each CTA of a block-scaled decode can find itself.
+int decode_run_list();
 // Tokens per decode tile of this shape.
 int decode_tile_tokens(int kvt, int dqk);
 

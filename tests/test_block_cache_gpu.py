@@ -265,6 +265,19 @@ def test_decode_long_sequences(fmt):
     ref.check(out, lse, ref.attend(c, c.cache, c.scales))
 
 
+@pytest.mark.parametrize("batch", [511, 700, 1300])
+def test_decode_many_sequences(batch):
+    """Runs found by each CTA (up to 512 sequences) and by the planner (more, in one round of
+    threads or two), over sequences of very different lengths, some empty, some windowed."""
+    lens = [(37 * i) % 90 if i % 11 else 0 for i in range(batch)]
+    lens[3], lens[-1] = 3000, 1500
+    for window in (-1, 60):
+        c = ref.make(fmt=INT8, kv_lens=lens, Hkv=2, group=3, d_qk=256, d_vo=256, page_size=16, bt=8, seed=42,
+                     window_left=window)
+        out, lse = decode(c)
+        ref.check(out, lse, ref.attend(c, c.cache, c.scales), f"window {window}")
+
+
 def test_decode_v_scales_over_the_whole_float_range():
     """Later blocks 2^100 above or below earlier ones, and blocks of zeros: the probabilities
     stay representable because they follow the largest V scale so far."""
