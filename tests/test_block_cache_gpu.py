@@ -446,6 +446,76 @@ def test_prefill_longer_than_the_probability_scratch():
     ref.check(out, lse, ref.attend(c, c.cache, c.scales))
 
 
+def test_pages_past_32_bit_offsets():
+    """Pages more than 2^32 bytes into the cache: append, decode, prefill by copy (limit raised)
+    and in the kernel (the default limit)."""
+    c = ref.make(fmt=INT8, kv_lens=[300, 130], qo_lens=[100, 130], n_new=[60, 130], Hkv=4, group=2, page_size=64, bt=16,
+                 seed=85)
+    n, first = 18000, 17000  # pages of 256 KiB
+    pages = first + torch.arange(c.num_pages)
+    cache = torch.zeros(n, c.cache.shape[1], dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(n, *c.scales.shape[1:], device="cuda")
+    cache[pages.cuda()], scales[pages.cuda()] = gpu(c.cache), gpu(c.scales)
+    indices = gpu(c.kv_indices + np.int32(first))
+    args = (gpu(c.kv_indptr), indices, gpu(c.last))
+    pa.paged_attn_append_kv_block(gpu(c.k_new), gpu(c.v_new), gpu(c.append_indptr), cache, *args, scales, page_size=64,
+                                  block_tokens=16)
+    after = ref.append(c, c.cache, c.scales)
+    assert np.array_equal(cache[pages.cuda()].cpu().numpy(), after[0])
+    assert np.array_equal(scales[pages.cuda()].cpu().numpy(), after[1], equal_nan=True)
+    kw = dict(kwargs(c), num_pages=n, block_scales=scales)
+    want = ref.attend(c, *after)
+    for limit in (-1, 32 << 30):
+        pa.paged_attn_set_prefill_dequant_limit(limit)
+        try:
+            out, lse = pa.paged_attn_prefill(gpu(c.q), gpu(c.qo_indptr), cache, *args, **kw)
+        finally:
+            pa.paged_attn_set_prefill_dequant_limit(-1)
+        assert ("dequant" in pa.paged_attn_last_variant()) == (limit > 0)
+        ref.check(out, lse, want, f"limit {limit}")
+    d = ref.SimpleNamespace(**vars(c))
+    d.qo_lens, d.qo_indptr, d.q = [1, 1], np.array([0, 1, 2], np.int32), c.q[[99, 229]]
+    out, lse = pa.paged_attn_decode(gpu(d.q), cache, *args, **kw)
+    ref.check(out, lse, ref.attend(d, *after))
+    pa.paged_attn_release_workspace()  # (the copy took gigabytes)
+
+
+def test_binding_refusals():
+    """What the Python calls refuse, with nothing launched."""
+    c = ref.make(fmt=INT8, kv_lens=[40], n_new=[40], Hkv=2, group=2, page_size=16, bt=8, seed=86)
+    q, cache, scales = gpu(c.q), gpu(c.cache), gpu(c.scales)
+    ip, ix, last, ai, k, v = (gpu(x) for x in (c.kv_indptr, c.kv_indices, c.last, c.append_indptr, c.k_new, c.v_new))
+    kw = kwargs(c)
+
+    def dec(**more):
+        return pa.paged_attn_decode(more.pop("q", q), cache, ip, ix, last, **{**kw, "block_scales": scales, **more})
+
+    def app(**more):
+        a = dict(k=k, v=v, ai=ai, cache=cache, ip=ip, scales=scales, ps=16, bt=8, fmt=INT8)
+        a.update(more)
+        pa.paged_attn_append_kv_block(a["k"], a["v"], a["ai"], a["cache"], a["ip"], ix, last, a["scales"], page_size=a["ps"],
+                                      block_tokens=a["bt"], kv_dtype=a["fmt"])
+
+    for bad in (dict(block_scales=None), dict(block_scales=scales.double()), dict(block_scales=scales[:-1]),
+                dict(block_scales=scales.cpu()), dict(block_tokens=0), dict(block_tokens=32), dict(block_tokens=3),
+                dict(q=q[:, :, ::2]), dict(q=q[0])):
+        with pytest.raises(ValueError):
+            dec(**bad)
+    many = torch.zeros(4096, device="cuda")
+    for bad in (dict(block_tokens=3, block_scales=many), dict(sm_scale=float("inf")), dict(kv_dtype=9)):
+        with pytest.raises(pa.PagedAttnError):
+            dec(**bad)
+    for bad in (dict(k=k.float()), dict(v=v[:-1]), dict(ai=ai.long()), dict(ip=ip[:1]), dict(scales=None),
+                dict(scales=scales.half()), dict(k=k.transpose(0, 1).contiguous().transpose(0, 1)), dict(bt=17)):
+        with pytest.raises(ValueError):
+            app(**bad)
+    with pytest.raises(pa.PagedAttnError):
+        app(fmt=pa.PA_KV_FP8_E4M3)
+    with pytest.raises(TypeError):
+        app(ai=[0, 40])
+    assert np.array_equal(cache.cpu().numpy(), c.cache)
+
+
 # ------------------------------------------------------------------------------ together
 class Server:
     """Requests on block-table rows, pages on a free list, an int8 / e4m3 cache: the state of a

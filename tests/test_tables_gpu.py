@@ -180,3 +180,24 @@ def test_build_reports_bad_entries():
 def test_build_of_an_empty_batch():
     got = run_build(np.zeros((2, 3), np.int32), np.zeros(0, np.int32), np.zeros(2, np.int32), np.zeros(0, np.int32), 16, 4, 2, 3)
     assert got == [[0], [-9, -9], [], [0], [-1] * 3, [-1] * 3] and pa.paged_attn_check_device_error() == 0
+
+
+def test_binding_refusals():
+    t, n = gpu(np.zeros((2, 3))), gpu(np.zeros(2))
+    for bad in (dict(t=t.long()), dict(t=t.t()), dict(t=t.cpu()), dict(t=t[0]), dict(lens=n[:1]), dict(lens=n.long()),
+                dict(ids=n[:1]), dict(free=n.float()), dict(count=n[:0])):
+        a = dict(t=t, ids=None, lens=n, free=n, count=n)
+        a.update(bad)
+        with pytest.raises(ValueError):
+            pa.paged_attn_resize_tables(a["t"], a["ids"], a["lens"], n, a["free"], a["count"], page_size=16)
+    out = pa.paged_attn_build_tables(t, None, n, n, page_size=16, num_pages=4, max_indices=2, num_tokens=3)
+    assert [x.numel() for x in out] == [3, 2, 2, 3, 3, 3] and out[4].dtype == torch.int64
+    for bad in (out[:5], list(out), (*out[:4], out[5], out[4]), (out[0][:1], *out[1:])):
+        with pytest.raises(ValueError):
+            pa.paged_attn_build_tables(t, None, n, n, page_size=16, num_pages=4, max_indices=2, num_tokens=3, out=bad)
+    for bad in (dict(page_size=24), dict(num_pages=0)):
+        kw = dict(page_size=16, num_pages=4, max_indices=2, num_tokens=3)
+        kw.update(bad)
+        with pytest.raises(pa.PagedAttnError):
+            pa.paged_attn_build_tables(t, None, n, n, **kw)
+    assert pa.paged_attn_check_device_error() == 0
