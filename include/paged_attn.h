@@ -63,8 +63,10 @@
  * captured into a CUDA graph allocates nothing: it uses the capturing stream's workspace
  * if that is large enough, else the legacy default stream's, else it fails with
  * PA_ERR_CUDA; so make an eager call of the same shape on one of those streams before
- * capturing.  The graph keeps that workspace's address, and replays share it with the
- * eager calls on its stream.
+ * capturing.  The graph keeps that workspace's address (the memory stays allocated, when a
+ * later call needs a larger one too, until paged_attn_release_workspace, after which the graph
+ * must not be replayed), and replays share it with the eager calls on its stream and with other
+ * graphs captured on it: those must not run at the same time.
  *
  * Errors: every entry point returns 0 (PA_OK) or a negative pa_status, and launches
  * nothing when it rejects its arguments.
@@ -116,7 +118,9 @@ typedef enum {
  *                   K^ = code(K) * block_scales[page][0][head][slot / block_tokens]
  *                   (likewise V), code an int8 or an e4m3 value.  4-byte aligned.  k_scale,
  *                   v_scale and sf are ignored.  Scales of blocks without a token are not
- *                   used (they may hold anything). */
+ *                   used (they may hold anything).  As with the other dtypes, a NaN among the
+ *                   V of a sequence's tokens (an e4m3 code; no int8 code is one) also reaches
+ *                   rows that do not see its token, if they see one of the same tile. */
 typedef struct {
   const float* k_scale;
   const float* v_scale;

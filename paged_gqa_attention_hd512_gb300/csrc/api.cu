@@ -54,6 +54,8 @@ constexpr int kMaxDevices = 64;
 struct Workspace {
   void* base = nullptr;
   size_t bytes = 0;
+  bool captured = false;       // a graph has its address
+  std::vector<void*> retired;  // smaller ones whose address a graph has
 };
 // one grow-only workspace per (device, stream): calls on different streams may overlap on
 // the GPU, calls on one stream are ordered by it
@@ -115,7 +117,10 @@ void* workspace(size_t need, cudaStream_t stream, int* status) {
     // warm-up call on that stream has grown), else an error
     for (cudaStream_t key : {stream, static_cast<cudaStream_t>(nullptr)}) {
       const auto it = g_ws[dev].find(key);
-      if (it != g_ws[dev].end() && it->second.bytes >= need) return it->second.base;
+      if (it != g_ws[dev].end() && it->second.bytes >= need) {
+        it->second.captured = true;
+        return it->second.base;
+      }
     }
     *status = PA_ERR_CUDA;
     return nullptr;
@@ -131,10 +136,12 @@ void* workspace(size_t need, cudaStream_t stream, int* status) {
       *status = PA_ERR_CUDA;
       return nullptr;
     }
-    cudaFree(w.base);
+    if (w.captured) w.retired.push_back(w.base);  // replays write to it until the workspaces are released
+    else cudaFree(w.base);
   }
   w.base = nullptr;
   w.bytes = 0;
+  w.captured = false;
   size_t bytes = align_up(need + need / 4, 1 << 20);
   if (cudaMalloc(&w.base, bytes) != cudaSuccess) {
     cudaGetLastError();
@@ -261,10 +268,10 @@ bool decode_direct(int kvt, int dqk, int dvo, int page_size, long long num_pages
 
 // Block-scaled decode: the equal runs that each kv head's pages are cut into (see
 // DecodeParams::shares), as many as the SMs serve at once; 0 (the chunks of the other dtypes)
-// with a forced chunk size or where the kv heads would leave over a tenth of the SMs idle.  With several chunks of unequal
-// sequences a CTA, their sums differ by a few tens of percent between CTAs, and the slowest
-// sets the time: 64 sequences of 1024 to 8192 tokens, 4 kv heads of int8, 192 us; in equal
-// runs 175 us (32768 tokens x 16 of e4m3: 330 and 312 us).
+// with a forced chunk size or where the kv heads would leave over a tenth of the SMs idle.
+// With several chunks of unequal sequences a CTA, their sums differ by a few tens of percent
+// between CTAs, and the slowest sets the time: 64 sequences of 1024 to 8192 tokens, 4 kv heads
+// of int8, 192 us; in equal runs 172 us (32768 tokens x 16 of e4m3: 330 and 306 us).
 int decode_shares(int kvt, bool direct, int hkv, int max_shares, int sms) {
   if (!kv_block_scaled(kvt) || direct || g_forced_chunk_pages > 0) return 0;
   const int shares = std::min(sms / hkv, max_shares);
@@ -496,8 +503,12 @@ int paged_attn_release_workspace(void) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return PA_ERR_CUDA;
   std::lock_guard<std::mutex> lock(g_ws_mutex);
-  for (auto& kv : g_ws[dev])
-    if (kv.second.base && cudaFree(kv.second.base) != cudaSuccess) return PA_ERR_CUDA;
+  for (auto& kv : g_ws[dev]) {
+    kv.second.retired.push_back(kv.second.base);
+    kv.second.base = nullptr;
+    for (; !kv.second.retired.empty(); kv.second.retired.pop_back())
+      if (cudaFree(kv.second.retired.back()) != cudaSuccess) return PA_ERR_CUDA;
+  }
   g_ws[dev].clear();
   return PA_OK;
 }
@@ -546,10 +557,13 @@ int paged_attn_check_device_error(int* code) {
   {
     std::lock_guard<std::mutex> lock(g_ws_mutex);
     for (auto& kv : g_ws[dev]) {
-      if (!kv.second.base) continue;
-      const int w = take_error_word(kv.second.base);
-      if (w < 0) return PA_ERR_CUDA;
-      if (v == 0) v = w;
+      std::vector<void*> bases = kv.second.retired;
+      if (kv.second.base) bases.push_back(kv.second.base);
+      for (void* base : bases) {
+        const int w = take_error_word(base);
+        if (w < 0) return PA_ERR_CUDA;
+        if (v == 0) v = w;
+      }
     }
   }
   {
@@ -612,7 +626,7 @@ int paged_attn_decode(const void* q, const void* kv_cache, const int32_t* kv_ind
   const size_t o_chunks = off; off = align_up(off + (size_t)max_chunks * sizeof(DecodeChunk), 256);
   const size_t o_seq = off; off = align_up(off + (size_t)batch * sizeof(int2), 256);
   const int shares = decode_shares(kv_dtype, direct, num_kv_heads, max_chunks - batch, sms);
-  const size_t o_run = off; off = align_up(off + (size_t)(shares + 1) * sizeof(int), 256);
+  const size_t o_run = off; off = align_up(off + (shares > 0 ? (size_t)(shares + 1) * sizeof(int) : 0), 256);
   const size_t o_ml = off; off = align_up(off + (size_t)max_chunks * num_qo_heads * sizeof(float2), 256);
   const size_t o_o = off; off = align_up(off + (size_t)max_chunks * num_qo_heads * head_dim_vo * sizeof(float), 256);
   char* ws = static_cast<char*>(workspace(off, static_cast<cudaStream_t>(stream), &st));
@@ -639,6 +653,7 @@ int paged_attn_decode(const void* q, const void* kv_cache, const int32_t* kv_ind
   p.ws_ml = reinterpret_cast<float2*>(ws + o_ml);
   p.ws_o = reinterpret_cast<float*>(ws + o_o);
   p.batch = batch;
+  p.num_pages = num_pages;
   p.Hq = num_qo_heads;
   p.Hkv = num_kv_heads;
   p.group = group;
@@ -1122,8 +1137,8 @@ extern "C" int paged_attn_decode_noalloc(const void* q, const void* kv_cache, co
   const size_t cap = PA_NOALLOC_SCRATCH_BYTES;
   const size_t per_chunk =
       sizeof(DecodeChunk) + (size_t)num_qo_heads * sizeof(float2) + (size_t)num_qo_heads * head_dim_vo * 4;
-  const size_t fixed = kFixedBytes + 256 + align_up((size_t)batch * sizeof(int2), 256) +
-                       align_up((size_t)(sms + 1) * sizeof(int), 256) + 4 * 256;
+  const size_t runs = kv_block_scaled(kv_dtype) ? align_up((size_t)(sms + 1) * sizeof(int), 256) : 0;
+  const size_t fixed = kFixedBytes + 256 + align_up((size_t)batch * sizeof(int2), 256) + runs + 4 * 256;
   if (fixed >= cap) return PA_ERR_SCRATCH;
   const long fit = (long)((cap - fixed) / per_chunk) - batch;
   const int forced = g_forced_chunk_pages;
@@ -1138,7 +1153,7 @@ extern "C" int paged_attn_decode_noalloc(const void* q, const void* kv_cache, co
   const size_t o_chunks = off; off = align_up(off + (size_t)max_chunks * sizeof(DecodeChunk), 256);
   const size_t o_seq = off; off = align_up(off + (size_t)batch * sizeof(int2), 256);
   const int shares = decode_shares(kv_dtype, direct, num_kv_heads, max_chunks - batch, sms);
-  const size_t o_run = off; off = align_up(off + (size_t)(shares + 1) * sizeof(int), 256);
+  const size_t o_run = off; off = align_up(off + (shares > 0 ? (size_t)(shares + 1) * sizeof(int) : 0), 256);
   const size_t o_ml = off; off = align_up(off + (size_t)max_chunks * num_qo_heads * sizeof(float2), 256);
   const size_t o_o = off; off = align_up(off + (size_t)max_chunks * num_qo_heads * head_dim_vo * sizeof(float), 256);
   if (off > cap) return PA_ERR_SCRATCH;
@@ -1180,6 +1195,7 @@ extern "C" int paged_attn_decode_noalloc(const void* q, const void* kv_cache, co
   p.ws_ml = reinterpret_cast<float2*>(ws + o_ml);
   p.ws_o = reinterpret_cast<float*>(ws + o_o);
   p.batch = batch;
+  p.num_pages = num_pages;
   p.Hq = num_qo_heads;
   p.Hkv = num_kv_heads;
   p.group = group;

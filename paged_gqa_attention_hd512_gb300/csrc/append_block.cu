@@ -89,11 +89,11 @@ __device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio) {
 }
 
 constexpr int kStepWarps = 8;  // warps per CTA of append_step_kernel
-constexpr int kRegs = 4;  // 16-element pieces of a block's new rows that a thread keeps
+constexpr int kRegs = 4;       // 16-element pieces of a block's new rows that a thread keeps
 
-// Long appends in blocks of two or four tokens, fewer than a TMA box.  A group of G threads (a power of two,
-// at least a warp) takes the blocks whose first new row lies among a block's worth of
-// consecutive new rows, for one kv head and side; blockDim.x / G groups per CTA.
+// Long appends in blocks of two or four tokens, fewer than a TMA box.  A group of G threads (a
+// power of two, at least a warp) takes the blocks whose first new row lies among a block's
+// worth of consecutive new rows, for one kv head and side; blockDim.x / G groups per CTA.
 template <int KVT>
 __global__ void __launch_bounds__(512, 2) append_block_kernel(const AppendBlockParams p, const int G) {
   __shared__ uint32_t s_max[2][32];  // per warp, in turn: the largest magnitude
@@ -130,13 +130,13 @@ __global__ void __launch_bounds__(512, 2) append_block_kernel(const AppendBlockP
       while (hi - lo > 1) {
         const int step = (hi - lo + 31) / 32;
         const int c = lo + step * lane;
-        const bool le = lane > 0 && c < hi && __ldg(p.append_indptr + c) <= i;
+        const bool le = lane > 0 && c < hi && p.append_indptr[c] <= i;
         const unsigned m = __ballot_sync(0xffffffffu, le);
         if (m) lo += step * (31 - __clz(m));
         hi = min(hi, lo + step);
       }
-      enter(lo, __ldg(p.append_indptr + lo), __ldg(p.append_indptr + lo + 1), __ldg(p.kv_indptr + lo),
-            __ldg(p.kv_indptr + lo + 1), __ldg(p.kv_last_page_len + lo));
+      enter(lo, p.append_indptr[lo], p.append_indptr[lo + 1], p.kv_indptr[lo], p.kv_indptr[lo + 1],
+            p.kv_last_page_len[lo]);
       if (i < a0 || i >= a_end) return;  // rows past the last sequence
     }
     const int t = kv_len - n_new + (i - a0);  // position in the sequence
@@ -151,12 +151,12 @@ __global__ void __launch_bounds__(512, 2) append_block_kernel(const AppendBlockP
       i += n;
       continue;
     }
-    const int page = __ldg(p.kv_indices + ip0 + t / ps);
+    const int page = p.kv_indices[ip0 + t / ps];
     const uint16_t* src = x0 + (size_t)i * row_elems;
     const int pieces = n << lrow;
     auto load = [&](int u, uint32_t* w) {
       const uint4* q = reinterpret_cast<const uint4*>(src + (size_t)(u >> lrow) * row_elems) + 2 * (u & ((1 << lrow) - 1));
-      const uint4 a = __ldg(q), c = __ldg(q + 1);
+      const uint4 a = q[0], c = q[1];
       w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
       w[4] = c.x, w[5] = c.y, w[6] = c.z, w[7] = c.w;
     };
@@ -247,10 +247,10 @@ __global__ void __launch_bounds__(512, 2) append_block_kernel(const AppendBlockP
 
 // ---------------------------------------------------------------------------------------
 // Short appends (a decode step's, few new rows a sequence) and blocks of one token: a warp per
-// (new row, kv head), K and V together.  What takes time is the chain of dependent loads, so the row's values are loaded
-// at once, beside the guess that row i belongs to sequence i; then the page id, then the old
-// scales.  A warp whose row is not its block's first new one leaves; one whose block has more
-// new rows reads those too.
+// (new row, kv head), K and V together.  What takes time is the chain of dependent loads, so
+// the row's values are loaded at once, beside the guess that row i belongs to sequence i; then
+// the page id, then the old scales.  A warp whose row is not its block's first new one leaves;
+// one whose block has more new rows reads those too.
 template <int KVT>
 __global__ void __launch_bounds__(32 * kStepWarps, 4) append_step_kernel(const AppendBlockParams p) {
   const int lane = threadIdx.x & 31;
@@ -265,32 +265,32 @@ __global__ void __launch_bounds__(32 * kStepWarps, 4) append_step_kernel(const A
   auto load_row = [&](int side, int r, uint4* w) {
     const int d = side ? p.d_vo : p.d_qk;
     const uint4* src = reinterpret_cast<const uint4*>((side ? p.v_new : p.k_new) + ((size_t)r * p.Hkv + h) * d);
-    w[0] = __ldg(src + lane);
-    w[1] = d == 512 ? __ldg(src + lane + 32) : make_uint4(0, 0, 0, 0);
+    w[0] = src[lane];
+    w[1] = d == 512 ? src[lane + 32] : make_uint4(0, 0, 0, 0);
   };
   uint4 w[2][2];
   load_row(0, i, w[0]);
   load_row(1, i, w[1]);
   int b = min(i, p.batch - 1);
-  int a0 = __ldg(p.append_indptr + b), a_end = __ldg(p.append_indptr + b + 1);
-  int ip0 = __ldg(p.kv_indptr + b), ip1 = __ldg(p.kv_indptr + b + 1), last = __ldg(p.kv_last_page_len + b);
+  int a0 = p.append_indptr[b], a_end = p.append_indptr[b + 1];
+  int ip0 = p.kv_indptr[b], ip1 = p.kv_indptr[b + 1], last = p.kv_last_page_len[b];
   if (i < a0 || i >= a_end) {
     // the last sequence b with append_indptr[b] <= i, 32 candidates per round
     int lo = 0, hi = p.batch;
     while (hi - lo > 1) {
       const int step = (hi - lo + 31) / 32;
       const int c = lo + step * lane;
-      const bool le = lane > 0 && c < hi && __ldg(p.append_indptr + c) <= i;
+      const bool le = lane > 0 && c < hi && p.append_indptr[c] <= i;
       const unsigned m = __ballot_sync(0xffffffffu, le);
       if (m) lo += step * (31 - __clz(m));
       hi = min(hi, lo + step);
     }
     b = lo;
-    a0 = __ldg(p.append_indptr + b);
-    a_end = __ldg(p.append_indptr + b + 1);
-    ip0 = __ldg(p.kv_indptr + b);
-    ip1 = __ldg(p.kv_indptr + b + 1);
-    last = __ldg(p.kv_last_page_len + b);
+    a0 = p.append_indptr[b];
+    a_end = p.append_indptr[b + 1];
+    ip0 = p.kv_indptr[b];
+    ip1 = p.kv_indptr[b + 1];
+    last = p.kv_last_page_len[b];
     if (i < a0 || i >= a_end) return;  // rows past the last sequence
   }
   const int kv_len = ip1 > ip0 ? (ip1 - ip0 - 1) * ps + last : 0;
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(32 * kStepWarps, 4) append_step_kernel(const A
   const int in_blk = t & (bt - 1), slot = t & (ps - 1);
   if (i > a0 && in_blk > 0) return;  // not the block's first new row
   const int n = min(bt - in_blk, min(a_end, p.total_new) - i);
-  const int page = __ldg(p.kv_indices + ip0 + t / ps);
+  const int page = p.kv_indices[ip0 + t / ps];
   if (page < 0 || page >= p.num_pages) {
     if (lane == 0) record_error(p.data_err, SITE_APPEND_POS);
     return;
@@ -380,8 +380,8 @@ struct StreamBlock {
 
 template <int KVT>
 __global__ void __launch_bounds__(kConsumers + 32 * kProducers, 1)
-    append_stream_kernel(const __grid_constant__ AppendBlockMaps tm, const AppendBlockParams p, const int G, const int stages,
-                         const int stage_bytes, const long long units) {
+    append_stream_kernel(const __grid_constant__ AppendBlockMaps tm, const AppendBlockParams p, const int G,
+                         const int stages, const int stage_bytes, const long long units) {
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint32_t s_max[2][kConsumers / 32];
   __shared__ StreamBlock s_blk[kMaxStages];
@@ -417,7 +417,12 @@ __global__ void __launch_bounds__(kConsumers + 32 * kProducers, 1)
         phase ^= 1;
       }
       if (slot_s % kProducers != me) return true;
-      if (!mbar_wait(&s_empty[slot_s], parity, p.err, SITE_APPEND_RING)) return false;
+      if (!__all_sync(0xffffffffu, mbar_wait(&s_empty[slot_s], parity, p.err, SITE_APPEND_RING))) {
+        // (not in the first phase, whose slots are empty) no copy of this warp may still be on
+        // its way when the CTA ends: those of this phase before slot_s, of the last from it on
+        for (int k = me; k < stages; k += kProducers) mbar_wait(&s_full[k], k < slot_s ? parity ^ 1 : parity, nullptr, 0);
+        return false;
+      }
       const bool is_v = hs & 1;
       uint64_t* full = &s_full[slot_s];
       const uint32_t dst = smem_u32(ring) + slot_s * stage_bytes;
@@ -450,23 +455,23 @@ __global__ void __launch_bounds__(kConsumers + 32 * kProducers, 1)
           while (hi - lo > 1) {
             const int step = (hi - lo + 31) / 32;
             const int k = lo + step * lane;
-            const bool le = lane > 0 && k < hi && __ldg(p.append_indptr + k) <= i;
+            const bool le = lane > 0 && k < hi && p.append_indptr[k] <= i;
             const unsigned m = __ballot_sync(0xffffffffu, le);
             if (m) lo += step * (31 - __clz(m));
             hi = min(hi, lo + step);
           }
           b = lo;
-          a0 = __ldg(p.append_indptr + b);
-          a_end = __ldg(p.append_indptr + b + 1);
+          a0 = p.append_indptr[b];
+          a_end = p.append_indptr[b + 1];
           n_new = a_end - a0;
           a_end = min(a_end, p.total_new);
           if (i < a0 || i >= a_end) {  // rows past the last sequence
             more = false;
             break;
           }
-          ip0 = __ldg(p.kv_indptr + b);
-          const int np = __ldg(p.kv_indptr + b + 1) - ip0;
-          kv_len = np > 0 ? (np - 1) * ps + __ldg(p.kv_last_page_len + b) : 0;
+          ip0 = p.kv_indptr[b];
+          const int np = p.kv_indptr[b + 1] - ip0;
+          kv_len = np > 0 ? (np - 1) * ps + p.kv_last_page_len[b] : 0;
           q0 = -32;
         }
         const int t = kv_len - n_new + (i - a0);  // position in the sequence
@@ -482,21 +487,21 @@ __global__ void __launch_bounds__(kConsumers + 32 * kProducers, 1)
           if (q - q0 >= 32) {
             q0 = q;
             const long long first = (long long)(q + lane) << lbt;
-            my_page = first < kv_len ? __ldg(p.kv_indices + ip0 + (int)first / ps) : -1;
+            my_page = first < kv_len ? p.kv_indices[ip0 + (int)first / ps] : -1;
           }
           const int page = __shfl_sync(0xffffffffu, my_page, q - q0);
           if (page < 0 || page >= p.num_pages) {
             if (lane == 0) record_error(p.data_err, SITE_APPEND_POS);
           } else {
             for (int hs = hs0; hs < hs1; ++hs)
-              if (!__all_sync(0xffffffffu, put(page, t & (ps - 1), rows, hs, i))) return;
+              if (!put(page, t & (ps - 1), rows, hs, i)) return;
           }
         }
         i += rows;
       }
     }
     for (int k = 0; k < groups; ++k)  // the end, once for each group
-      if (!__all_sync(0xffffffffu, put(0, 0, 0, 0, 0))) return;
+      if (!put(0, 0, 0, 0, 0)) return;
     return;
   }
 
@@ -588,7 +593,11 @@ __global__ void __launch_bounds__(kConsumers + 32 * kProducers, 1)
   }
 }
 
-// Few new rows a sequence (a decode step's append)
+// Few new rows a sequence (a decode step's append).  In microseconds, a warp per row and head /
+// the long forms, new rows a sequence 1, 4, 8, 16: 64 sequences of 4 x (512 + 512) in blocks of
+// 16 2.9 / 18.1, 5.8 / 7.4, 10.6 / 7.8, 14.3 / 7.2; 256 of 1 x (256 + 256) in blocks of 64
+// 2.7 / 63.7, 6.0 / 18.7, 7.8 / 11.3, 13.3 / 7.8; 64 of 4 x (512 + 512) in blocks of 4
+// 2.9 / 8.7, 6.0 / 3.9, 6.6 / 3.9 (1 and 2 rows, which leave a block unfinished: 4.1 / 5.8).
 bool append_block_steps(int total_new, int batch) { return total_new <= 4ll * batch; }
 
 }  // namespace

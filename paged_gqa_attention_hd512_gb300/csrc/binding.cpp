@@ -115,16 +115,20 @@ void* stream_of(PyObject* o) {
 
 bool block_dtype(int kv_dtype) { return kv_dtype == PA_KV_INT8_BLOCK || kv_dtype == PA_KV_FP8_BLOCK; }
 
-// num_pages, None: as many as the cache holds.
+// num_pages, None: as many as the cache holds (and, for the block dtypes, at most that).
 int pages_of(PyObject* num_pages, PyObject* cache, int hkv, int dqk, int dvo, int ps, int kv_dtype) {
-  if (num_pages != Py_None) return integer(num_pages);
+  if (num_pages != Py_None && !block_dtype(kv_dtype)) return integer(num_pages);
   static const int x2[5] = {4, 2, 1, 2, 2};
   if (kv_dtype < 0 || kv_dtype > 4) bad(PyExc_KeyError, "unknown kv_dtype");
   const int64_t page = (int64_t)hkv * ps * (dqk + dvo) * x2[kv_dtype] / 2;
   if (page <= 0) bad(PyExc_ZeroDivisionError, "a page without bytes");
   const at::Tensor* t = tensor(cache);
   if (!t) bad(PyExc_ValueError, "kv_cache must be a tensor");
-  return int_of((int64_t)t->nbytes() / page);
+  const int64_t held = (int64_t)t->nbytes() / page;
+  if (num_pages == Py_None) return int_of(held);
+  const int given = integer(num_pages);
+  if (given > held) bad(PyExc_ValueError, "num_pages is more than kv_cache holds");
+  return given;
 }
 
 // The pointer of a block_scales pool, after checking that it covers the pages.

@@ -99,7 +99,9 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* e
 // serialization may start while the kernel before it on the stream still runs; it calls
 // grid_dep_wait() before touching global memory, which returns once that kernel has
 // completed and its writes are visible (at once when there is no such kernel).  A kernel
-// calls grid_dep_launch() to let its dependent start early.
+// calls grid_dep_launch() to let its dependent start early; what it writes after that call is
+// not read-only while the dependent runs, so a dependent reads such data with plain loads
+// (no __ldg, which may be moved before the wait).
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

@@ -499,9 +499,9 @@ __device__ __forceinline__ int decode_runs_of_cta(const DecodeParams& p, int run
   auto visible = [&](int b, int& first) -> int {
     first = 0;
     if (b >= p.batch) return 0;
-    const int np = max(0, __ldg(p.kv_indptr + b + 1) - __ldg(p.kv_indptr + b));
+    const int np = max(0, p.kv_indptr[b + 1] - p.kv_indptr[b]);
     if (np > 0 && p.window_left >= 0)
-      first = max(0, (np - 1) * ps + __ldg(p.kv_last_page_len + b) - 1 - p.window_left) / ps;
+      first = max(0, (np - 1) * ps + p.kv_last_page_len[b] - 1 - p.window_left) / ps;
     return np - first;
   };
   int units = 0;
@@ -546,8 +546,9 @@ __device__ __forceinline__ int decode_runs_of_cta(const DecodeParams& p, int run
     if (record && b < p.batch) p.seq_info[b] = make_int2(c0, n);
     const int k = run - e0 / S;
     if (k >= 0 && k < n)
-      list[atomicAdd(scratch + 48, 1)] = make_int4(b, first + max(e0, run * S) - e0, first + min(e0 + pages, (run + 1) * S) - e0,
-                                                   2 * (c0 + k) + (n == 1 ? 1 : 0));
+      list[atomicAdd(scratch + 48, 1)] =
+          make_int4(b, first + max(e0, run * S) - e0, first + min(e0 + pages, (run + 1) * S) - e0,
+                    2 * (c0 + k) + (n == 1 ? 1 : 0));
     unit0 += all_units;
     chunk0 += all_chunks;
     __syncthreads();  // the words may be written again
@@ -677,7 +678,8 @@ __global__ void __launch_bounds__(DecodeCfg<KVT, DQK, DVO>::THREADS, 1)
     if (warp == 9) {
       // ---------------------------------------------------------------- block scales
       // The K and V scale of each token of a tile into the tile's stage (0 past the end of
-      // the sequence and before the window, whatever the pool holds there), two tokens per lane, and the tile's largest V scale.  Page ids are
+      // the sequence and before the window, whatever the pool holds there, and for page ids
+      // out of range), two tokens per lane, and the tile's largest V scale.  Page ids are
       // fetched two tiles ahead and scales one tile ahead of the wait for the stage, so the
       // two dependent loads behind a scale are off the consumers' path.
       float* sc0 = reinterpret_cast<float*>(smem + L::OFF_SC);
@@ -697,18 +699,18 @@ __global__ void __launch_bounds__(DecodeCfg<KVT, DQK, DVO>::THREADS, 1)
 #pragma unroll
           for (int k = 0; k < T / 32; ++k) {
             const int tok = tok0 + lane + 32 * k;
-            page[k] = tok < tok_end && tok >= win_lo ? __ldg(p.kv_indices + ip0 + (tok >> lps)) : -1;
+            page[k] = tok < tok_end && tok >= win_lo ? p.kv_indices[ip0 + (tok >> lps)] : -1;
           }
         };
         auto load_scales = [&](int tok0) {
 #pragma unroll
           for (int k = 0; k < T / 32; ++k) {
             ks[k] = vs[k] = 0.f;
-            if (page[k] >= 0) {
+            if ((unsigned)page[k] < (unsigned)p.num_pages) {
               const int blk = ((tok0 + lane + 32 * k) & (ps - 1)) >> p.bs.log2_tokens;
               const float* src = p.bs.s + ((size_t)page[k] * 2 * p.Hkv + kvh) * p.bs.per_head + blk;
-              ks[k] = __ldg(src);
-              vs[k] = __ldg(src + (size_t)p.Hkv * p.bs.per_head);
+              ks[k] = src[0];
+              vs[k] = src[(size_t)p.Hkv * p.bs.per_head];
             }
           }
         };
@@ -783,8 +785,7 @@ __global__ void __launch_bounds__(DecodeCfg<KVT, DQK, DVO>::THREADS, 1)
           const int h = nt * 8 + gid;
           uint32_t v = 0;
           if (h < gsz)
-            v = __ldg(reinterpret_cast<const uint32_t*>(qbase + (size_t)h * DQK +
-                                                        q_col<KVT>(dqk0, ks, hf, tig)));
+            v = *reinterpret_cast<const uint32_t*>(qbase + (size_t)h * DQK + q_col<KVT>(dqk0, ks, hf, tig));
           qf[ks][nt][hf] = v;
         }
     float sm_log2 = p.sm_scale * 1.4426950408889634f * kscale;

@@ -15,7 +15,8 @@ static cudaError_t run_decode(const DecodeLaunch& L) {
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sm::ALLOC);
   if (e != cudaSuccess) return e;
   // a programmatic dependent of the planner
-  return launch_pdl(kern, dim3(L.grid), dim3(DecodeCfg<KVT, DQK, DVO>::THREADS), Sm::ALLOC, L.stream, 1, L.tk, L.tv, L.tsfk, L.tsfv, L.p);
+  return launch_pdl(kern, dim3(L.grid), dim3(DecodeCfg<KVT, DQK, DVO>::THREADS), Sm::ALLOC, L.stream, 1, L.tk, L.tv,
+                    L.tsfk, L.tsfv, L.p);
 }
 
 template <int KVT>

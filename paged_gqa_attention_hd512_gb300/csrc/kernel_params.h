@@ -62,7 +62,7 @@ struct DecodeParams {
   int2* seq_info;     // per sequence: {first chunk row, number of chunks}
   float* ws_o;        // [max_chunks][Hq][d_vo] unnormalised partial outputs
   float2* ws_ml;      // [max_chunks][Hq] {running max (log2 units), running sum}
-  int batch, Hq, Hkv, group, page_size, window_left;
+  int batch, num_pages, Hq, Hkv, group, page_size, window_left;
   int max_chunks, target_chunks, forced_chunk_pages;
   int min_chunk_pages;  // pages of about 4 MiB of K and V of one kv head
   int grid;             // CTAs of the decode kernel

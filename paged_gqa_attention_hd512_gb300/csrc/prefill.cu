@@ -25,9 +25,10 @@ __global__ void __launch_bounds__(1024) prefill_prep_kernel(const PrefillParams 
 template <int KVT, bool PAD>
 static cudaError_t run_prep(int dqk, int dvo, int grid, const PrefillParams& p, const DequantParams& d,
                             cudaStream_t s) {
-  if (dqk == 512 && dvo == 512) return launch_pdl(prefill_prep_kernel<KVT, 512, 512, true, PAD>, dim3(grid), dim3(1024), 0, s, 1, p, d);
-  if (dqk == 512 && dvo == 256) return launch_pdl(prefill_prep_kernel<KVT, 512, 256, true, PAD>, dim3(grid), dim3(1024), 0, s, 1, p, d);
-  if (dqk == 256 && dvo == 256) return launch_pdl(prefill_prep_kernel<KVT, 256, 256, true, PAD>, dim3(grid), dim3(1024), 0, s, 1, p, d);
+  auto go = [&](auto kern) { return launch_pdl(kern, dim3(grid), dim3(1024), 0, s, 1, p, d); };
+  if (dqk == 512 && dvo == 512) return go(prefill_prep_kernel<KVT, 512, 512, true, PAD>);
+  if (dqk == 512 && dvo == 256) return go(prefill_prep_kernel<KVT, 512, 256, true, PAD>);
+  if (dqk == 256 && dvo == 256) return go(prefill_prep_kernel<KVT, 256, 256, true, PAD>);
   return cudaErrorInvalidValue;
 }
 

@@ -80,7 +80,7 @@ __device__ __forceinline__ void prefill_dequant_body(const DequantParams& d, int
       if (g >= total) break;
       const uint32_t e = (uint32_t)(g / units);
       const uint32_t u = (uint32_t)(g - (uint64_t)e * units);
-      page[k] = (size_t)__ldg(d.kv_indices + e);
+      page[k] = (size_t)d.kv_indices[e];
       uint32_t us = u;
       zero[k] = false;
       is_v[k] = u >= k_units;
@@ -95,13 +95,13 @@ __device__ __forceinline__ void prefill_dequant_body(const DequantParams& d, int
       if (zero[k]) continue;
       if constexpr (KVT == KV_BF16) {
         const uint4* src = reinterpret_cast<const uint4*>(d.cache + page[k] * in_page) + 2 * (size_t)us;
-        a8[k] = __ldg(src);
-        b8[k] = __ldg(src + 1);
+        a8[k] = src[0];
+        b8[k] = src[1];
       } else if constexpr (KVT != KV_NVFP4) {
-        a8[k] = __ldg(reinterpret_cast<const uint4*>(d.cache + page[k] * in_page) + us);
+        a8[k] = reinterpret_cast<const uint4*>(d.cache + page[k] * in_page)[us];
       } else {
-        a4[k] = __ldg(reinterpret_cast<const uint2*>(d.cache + page[k] * in_page) + us);
-        sb[k] = __ldg(d.sf + page[k] * units_in + us);
+        a4[k] = reinterpret_cast<const uint2*>(d.cache + page[k] * in_page)[us];
+        sb[k] = d.sf[page[k] * units_in + us];
       }
     }
 #pragma unroll

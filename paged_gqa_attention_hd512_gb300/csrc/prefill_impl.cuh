@@ -83,7 +83,8 @@ struct PrefillCfg {
   // into staging rings with TMA; the converters turn two staged halves into one slot of the
   // bf16 / f16 ring the MMAs read.  The staging rings hide the L2 latency, so the converted
   // ring only covers the conversion.
-  static constexpr int CW = KVT == KV_FP8 || kv_block_scaled(KVT) ? 64 : (KVT == KV_NVFP4 ? 32 : 0);  // packed bytes per key and half
+  // packed bytes per key and half
+  static constexpr int CW = KVT == KV_FP8 || kv_block_scaled(KVT) ? 64 : (KVT == KV_NVFP4 ? 32 : 0);
   static constexpr int STG_BYTES = N * CW;
   static constexpr int NQS = 2 * NQC, NVS = 2 * NVC;                         // staged halves per step
   static constexpr int SFW_K = DQK / 16, SFW_V = DVO / 16;                  // scale bytes per key

@@ -224,6 +224,26 @@ def test_bad_data_does_not_end_the_waits_of_later_calls():
     assert pa.paged_attn_check_device_error() == 401
 
 
+@pytest.mark.parametrize("bt", [8, 64])
+def test_append_after_a_wait_gave_up(bt):
+    """With the waits' error word set (here from the host) a streamed append gives up and
+    returns, with no copy of its ring still on the way; once the word is cleared the same
+    append is right."""
+    c = ref.make(fmt=INT8, kv_lens=[9000, 300], n_new=[9000, 300], Hkv=2, page_size=64, bt=bt, seed=12)
+    want = ref.append(c, c.cache, c.scales)
+    cache, scales = gpu(c.cache), gpu(c.scales)
+    args = (gpu(c.k_new), gpu(c.v_new), gpu(c.append_indptr), cache, gpu(c.kv_indptr), gpu(c.kv_indices), gpu(c.last),
+            scales)
+    assert pa.load().paged_attn_debug_set_error_word(0, 7) == pa.PA_OK
+    pa.paged_attn_append_kv_block(*args, page_size=64, block_tokens=bt)
+    assert pa.paged_attn_check_device_error() == 7
+    cache.copy_(gpu(c.cache))
+    scales.copy_(gpu(c.scales))
+    pa.paged_attn_append_kv_block(*args, page_size=64, block_tokens=bt)
+    assert np.array_equal(scales.cpu().numpy(), want[1], equal_nan=True)
+    assert np.array_equal(cache.cpu().numpy(), want[0])
+
+
 # ------------------------------------------------------------------------------ decode
 DECODES = [
     dict(kv_lens=[37, 64], Hkv=1, group=8, page_size=16, bt=16),
@@ -496,8 +516,8 @@ def test_binding_refusals():
         pa.paged_attn_append_kv_block(a["k"], a["v"], a["ai"], a["cache"], a["ip"], ix, last, a["scales"], page_size=a["ps"],
                                       block_tokens=a["bt"], kv_dtype=a["fmt"])
 
-    for bad in (dict(block_scales=None), dict(block_scales=scales.double()), dict(block_scales=scales[:-1]),
-                dict(block_scales=scales.cpu()), dict(block_tokens=0), dict(block_tokens=32), dict(block_tokens=3),
+    for bad in (dict(num_pages=len(c.cache) + 1), dict(block_scales=None), dict(block_scales=scales.double()),
+                dict(block_scales=scales[:-1]), dict(block_scales=scales.cpu()), dict(block_tokens=0), dict(block_tokens=32), dict(block_tokens=3),
                 dict(q=q[:, :, ::2]), dict(q=q[0])):
         with pytest.raises(ValueError):
             dec(**bad)
@@ -514,6 +534,29 @@ def test_binding_refusals():
     with pytest.raises(TypeError):
         app(ai=[0, 40])
     assert np.array_equal(cache.cpu().numpy(), c.cache)
+
+
+def test_a_graph_outlives_its_workspace_growing():
+    """A later call on the stream needs a larger workspace than the one whose address a graph
+    has: the graph's stays allocated, and its replays are right."""
+    c = ref.make(fmt=INT8, kv_lens=[3000, 41], Hkv=2, group=3, page_size=16, bt=8, seed=87)
+    q, cache, scales = gpu(c.q), gpu(c.cache), gpu(c.scales)
+    args = [gpu(x) for x in (c.kv_indptr, c.kv_indices, c.last)]
+    kw = dict(kwargs(c), block_scales=scales)
+    pa.paged_attn_release_workspace()
+    want, want_lse = pa.paged_attn_decode(q, cache, *args, **kw)
+    out, lse = torch.empty_like(want), torch.empty_like(want_lse)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        pa.paged_attn_decode(q, cache, *args, out=out, lse=lse, **kw)
+    big = ref.make(fmt=FP8, kv_lens=[6000, 5000], qo_lens=[700, 900], Hkv=4, group=4, page_size=32, bt=32, seed=88)
+    prefill(big)
+    keep = [torch.full((1 << 20,), 9, dtype=torch.int32, device="cuda") for _ in range(8)]  # whatever was freed is used
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    assert all(bool((t == 9).all()) for t in keep)
+    assert pa.paged_attn_check_device_error() == 0
 
 
 # ------------------------------------------------------------------------------ together
