@@ -392,6 +392,22 @@ def test_prefill_extend_splits_the_prefix(shape, fmt):
         ref.check(out, lse, want, f"limit {limit}")
 
 
+@pytest.mark.parametrize("fmt", [INT8, FP8])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_prefill_in_the_kernel_again_and_again(shape, fmt):
+    """The converters' staging ring under load: the same bits every time."""
+    c = ref.make(fmt=fmt, kv_lens=[5120, 2500], qo_lens=[20, 33], Hkv=2, group=4, d_qk=shape[0], d_vo=shape[1],
+                 page_size=32, bt=16, seed=89)
+    want = ref.attend(c, c.cache, c.scales)
+    pa.paged_attn_set_prefill_dequant_limit(0)
+    try:
+        runs = [prefill(c) for _ in range(12)]
+    finally:
+        pa.paged_attn_set_prefill_dequant_limit(-1)
+    ref.check(*runs[0], want)
+    assert all(torch.equal(o, runs[0][0]) and torch.equal(l, runs[0][1]) for o, l in runs[1:])
+
+
 @pytest.mark.parametrize("order", [1, -1])
 @pytest.mark.parametrize("shape", [(512, 512), (256, 256)])
 def test_prefill_v_scales_over_the_whole_float_range(shape, order):
