@@ -177,8 +177,9 @@ int paged_attn_decode(const void* q, const void* kv_cache, const int32_t* kv_ind
  * that pads each page to 8 rows per kv head (num_pages * num_kv_heads * 8 *
  * (head_dim_qk + head_dim_vo) * 2 bytes), under the same limit; beyond it the call
  * returns PA_ERR_UNSUPPORTED.  The block dtypes follow the same rules, except that a batch
- * with at most 128 / group new tokens a sequence on average (a query tile) is always
- * converted inside the kernel (page sizes of 8 and more): their copy holds the codes' values
+ * with at most 256 / group new tokens a sequence on average (two query tiles; one, 128 / group,
+ * for head_dim_vo 512) is always converted inside the kernel (page sizes of 8 and more): their
+ * copy holds the codes' values
  * (K in bf16, V in f16, both exact), and the scales are applied to scores and probabilities
  * as in paged_attn_decode.  When the
  * (query tile, kv head) items are fewer than the SMs (a few new tokens over a long

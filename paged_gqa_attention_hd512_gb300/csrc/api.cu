@@ -719,14 +719,16 @@ int prefill_call(const void* q, const int32_t* qo_indptr, int total_q, const voi
   // inside the kernel
   const bool quant = kv_dtype != PA_KV_BF16, scaled = kv_block_scaled(kv_dtype);
   const uint64_t bf16_page = (uint64_t)num_kv_heads * rows_copy * (head_dim_qk + head_dim_vo) * 2;
-  // Codes with block scales are converted in the kernel where the batch has at most a query
-  // tile a sequence: each KV tile is then converted once, and the copy (a byte read, two
-  // written and two read again per element) only costs.  4 sequences of 16384 tokens with 4
-  // new ones, 2 kv heads of 512 / 256: copy 97 us, in the kernel 65; with 32 new ones (two
-  // tiles) 119 and 117, with 64 179 and 228; head_dim_vo 512 (two passes): 133 and 120, 174
-  // and 232, 266 and 457.
-  const bool one_tile = scaled && !pad && total_q <= (long long)batch * rows_per_tile;
-  const bool dequant = (quant || pad) && !one_tile && (uint64_t)num_pages * bf16_page <= g_prefill_dequant_limit.load();
+  // Codes with block scales are converted in the kernel where each KV tile is read at most
+  // twice (query tiles a sequence x passes of 256 output columns): the copy (a byte read, two
+  // written and two read again per element) costs more than the second conversion.  4 x 16000
+  // cached tokens, 2 kv heads of group 8, 4 new tokens: copy 104 us, in the kernel 59; 32 (two
+  // tiles) 119 and 100; 48 135 and 136; head_dim_vo 512 (two passes) with 4, 32: 148 and 108,
+  // 177 and 190.  16 sequences of 2000 to 6000: 111 and 78, 157 and 163, 194 and 253; 160 and
+  // 148, 231 and 321.
+  const int passes = head_dim_vo > 256 ? 2 : 1;
+  const bool few_visits = scaled && !pad && (long long)total_q * passes <= 2ll * batch * rows_per_tile;
+  const bool dequant = (quant || pad) && !few_visits && (uint64_t)num_pages * bf16_page <= g_prefill_dequant_limit.load();
   if (pad && !dequant) return PA_ERR_UNSUPPORTED;  // the padded copy would exceed the limit
   const int run_kvt = dequant ? (int)PA_KV_BF16 : kv_dtype;
   const int smem = scaled ? prefill_block_smem_bytes(run_kvt, head_dim_qk, head_dim_vo)

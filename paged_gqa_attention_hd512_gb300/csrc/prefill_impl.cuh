@@ -33,6 +33,8 @@
 // half of every K/V tile (see PrefillCfg).
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "tc_helpers.cuh"
 
@@ -1082,26 +1084,34 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DVO, KVT, PAIR, SC>::THREADS, 
           if (half == 0) mbar_wait(&kv_empty[slot], ((rj / NSLOT) & 1) ^ 1, p.err, SITE_PRE_KV_EMPTY);
           __syncwarp();
           uint8_t* sp = smem + C::OFF_RING + slot * C::CHUNK + half * C::HALF + t * 128;
+          // (K and V apart: a select between the two forms would compute both)
+          auto convert = [&](auto to_f16) {
 #pragma unroll
-          for (int jj = 0; jj < 8; ++jj) {  // 16-byte output chunk jj = elements 8jj .. 8jj+7
-            uint32_t w[4];
+            for (int jj = 0; jj < 8; ++jj) {  // 16-byte output chunk jj = elements 8jj .. 8jj+7
+              uint32_t w[4];
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const uint32_t r = w16[2 * jj + q];
-              if (KVT == KV_INT8B) {
-                w[2 * q] = is_v ? i8_biased_pair_f16x2<0, 1>(r ^ 0x80808080u) : i8_pair_bf16x2<0, 1>(r);
-                w[2 * q + 1] = is_v ? i8_biased_pair_f16x2<2, 3>(r ^ 0x80808080u) : i8_pair_bf16x2<2, 3>(r);
-              } else {
-                w[2 * q] = e4m3x2_to_f16x2(r & 0xFFFFu);
-                w[2 * q + 1] = e4m3x2_to_f16x2(r >> 16);
-                if (!is_v) {
-                  w[2 * q] = f16x2_to_bf16x2(w[2 * q]);
-                  w[2 * q + 1] = f16x2_to_bf16x2(w[2 * q + 1]);
+              for (int q = 0; q < 2; ++q) {
+                const uint32_t r = w16[2 * jj + q];
+                if constexpr (KVT == KV_INT8B && to_f16) {
+                  w[2 * q] = i8_biased_pair_f16x2<0, 1>(r ^ 0x80808080u);
+                  w[2 * q + 1] = i8_biased_pair_f16x2<2, 3>(r ^ 0x80808080u);
+                } else if constexpr (KVT == KV_INT8B) {
+                  w[2 * q] = i8_pair_bf16x2<0, 1>(r);
+                  w[2 * q + 1] = i8_pair_bf16x2<2, 3>(r);
+                } else {
+                  w[2 * q] = e4m3x2_to_f16x2(r & 0xFFFFu);
+                  w[2 * q + 1] = e4m3x2_to_f16x2(r >> 16);
+                  if constexpr (!to_f16) {
+                    w[2 * q] = f16x2_to_bf16x2(w[2 * q]);
+                    w[2 * q + 1] = f16x2_to_bf16x2(w[2 * q + 1]);
+                  }
                 }
               }
+              *reinterpret_cast<uint4*>(sp + ((jj ^ (t & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            *reinterpret_cast<uint4*>(sp + ((jj ^ (t & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+          };
+          if (is_v) convert(std::true_type{});
+          else convert(std::false_type{});
           if (half == 1) fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
