@@ -179,9 +179,8 @@ int paged_attn_decode(const void* q, const void* kv_cache, const int32_t* kv_ind
  * returns PA_ERR_UNSUPPORTED.  The block dtypes follow the same rules, except that a batch
  * with at most 256 / group new tokens a sequence on average (two query tiles; one, 128 / group,
  * for head_dim_vo 512) is always converted inside the kernel (page sizes of 8 and more): their
- * copy holds the codes' values
- * (K in bf16, V in f16, both exact), and the scales are applied to scores and probabilities
- * as in paged_attn_decode.  When the
+ * copy holds the codes' values (K in bf16, V in f16, both exact), and the scales are applied
+ * to scores and probabilities as in paged_attn_decode.  When the
  * (query tile, kv head) items are fewer than the SMs (a few new tokens over a long
  * prefix), the device planner may split long KV ranges into chunks whose fp32 partials a
  * merge kernel combines (paged_attn_set_prefill_split_kv); the workspace then also holds

@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillParams 
           for (int b = 0; b < B; ++b)
 #pragma unroll
             for (int k = 0; k < G4; ++k)
-              v[b][k] = k0 + b < cnt ? __ldg(src + (size_t)(s0 + k0 + b) * step + 32 * k) : make_float4(0.f, 0.f, 0.f, 0.f);
+              v[b][k] = k0 + b < cnt ? src[(size_t)(s0 + k0 + b) * step + 32 * k] : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int b = 0; b < B; ++b) {
             const float wb = __shfl_sync(0xffffffffu, w, (k0 + b) & 31);
